@@ -22,7 +22,9 @@ STATUS_NAMES = {0: "CSA_OK", 1: "CSA_ERR_INVALID_ARGUMENT", 2: "CSA_ERR_UNSUPPOR
                 3: "CSA_ERR_WORKSPACE_TOO_SMALL", 4: "CSA_ERR_CUDA", 5: "CSA_ERR_DEVICE_FAULT",
                 6: "CSA_ERR_TIMEOUT"}
 FLAG_PAGE_OOB, FLAG_ROW_INVALID, FLAG_TOPK_OOB, FLAG_TIMEOUT, FLAG_APPEND = 0x1, 0x2, 0x4, 0x8, 0x10
+FLAG_NO_PAGES = 0x20
 OP_APPEND, OP_INDEX_SCORE, OP_TOPK, OP_SPARSE_ATTN, OP_DECODE = range(5)
+OP_DENSE_ATTN, OP_PAGES_RESERVE, OP_PAGES_FORK, OP_PAGES_FREE, OP_PAGES_COMPACT = range(5, 10)
 D, DI, TOPK, WINDOW, PAGE = 512, 128, 512, 128, 64
 KV_PAGE_BYTES, IDX_PAGE_BYTES = 18432, 4352
 
@@ -51,6 +53,10 @@ class CsaCompress(C.Structure):
 class CsaOpts(C.Structure):
     _fields_ = [("plan_in", C.c_void_p), ("plan_out", C.c_void_p), ("rope_cos", C.c_void_p),
                 ("rope_sin", C.c_void_p), ("rope_rows", C.c_int32), ("candidate_blocks", C.c_int32)]
+
+
+class CsaPages(C.Structure):
+    _fields_ = [("page_table", C.c_void_p), ("refs", C.c_void_p)]
 
 
 class CsaRows(C.Structure):
@@ -87,6 +93,11 @@ def lib():
             L.csa_topk_two_level.argtypes = [i32, vp, i32, vp, i32, i32, vp, vp, sz, vp]
             L.csa_sparse_attn_ex.argtypes = [vp, vp, vp, vp, i32, vp, f32, vp, vp, vp, vp, sz, vp]
             L.csa_decode_ex.argtypes = [vp, vp, vp, i32, vp, vp, i32, vp, f32, vp, vp, vp, vp, vp, sz, vp]
+            L.csa_dense_attn.argtypes = [vp, vp, vp, i32, vp, f32, vp, vp, vp, vp, sz, vp]
+            L.csa_pages_reserve.argtypes = [vp, vp, i32, vp, vp, vp, i32, vp, sz, vp]
+            L.csa_pages_fork.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+            L.csa_pages_free.argtypes = [vp, vp, i32, vp, vp, vp, sz, vp]
+            L.csa_pages_compact.argtypes = [vp, vp, vp, vp, vp, sz, vp]
             L.csa_check_device_status.argtypes = [vp, vp, C.POINTER(C.c_uint32)]
             L.csa_set_wait_budget.argtypes = [C.c_int64]
             L.csa_status_string.argtypes = [i32]
@@ -94,7 +105,8 @@ def lib():
             for fn in ("csa_append", "csa_append_compress", "csa_index_score", "csa_topk", "csa_sparse_attn",
                        "csa_decode", "csa_step", "csa_index_score_noalloc", "csa_check_device_status",
                        "csa_set_wait_budget", "csa_sparse_attn_ex", "csa_decode_ex", "csa_step_ex",
-                       "csa_topk_two_level"):
+                       "csa_topk_two_level", "csa_dense_attn", "csa_pages_reserve", "csa_pages_fork",
+                       "csa_pages_free", "csa_pages_compact"):
                 getattr(L, fn).restype = C.c_int
             _lib = L
     return _lib
@@ -253,6 +265,54 @@ def csa_step(cache, window, pos0, tok_off, total_tokens, kv_in, idx_in, pending,
     _check(rc, "csa_step")
 
 
+def csa_dense_attn(cache, window, rows, n_heads, q, softmax_scale, out, lse, opts, ws, stream=None):
+    """Attention over every visible entry and the window (opts: rotary tables or None)."""
+    rc = lib().csa_dense_attn(C.byref(cache), C.byref(window) if window is not None else None, C.byref(rows),
+                              int(n_heads), _ptr(q), float(softmax_scale), _ptr(out), _ptr(lse), _opt(opts),
+                              _ptr(ws), _nbytes(ws), _stream(stream))
+    _check(rc, "csa_dense_attn")
+
+
+# ---- page management -----------------------------------------------------------------
+def make_pages(page_table, refs):
+    """The cache's page table (int32, writable) and each page's count (int32 [num_pages])."""
+    return CsaPages(_ptr(page_table), _ptr(refs))
+
+
+def _same_length(where, n, *lists):
+    """Every list of a page call has an element for each of its n requests."""
+    if any(t is not None and t.numel() < n for t in lists):
+        raise CsaError(1, where)
+
+
+def csa_pages_reserve(cache, pages, req, first, count, max_count, ws, stream=None):
+    _same_length("csa_pages_reserve", req.numel(), first, count)
+    rc = lib().csa_pages_reserve(C.byref(cache), C.byref(pages), int(req.numel()), _ptr(req), _ptr(first),
+                                 _ptr(count), int(max_count), _ptr(ws), _nbytes(ws), _stream(stream))
+    _check(rc, "csa_pages_reserve")
+
+
+def csa_pages_fork(cache, pages, window, pending, parent, child, entries, ws=None, stream=None):
+    _same_length("csa_pages_fork", child.numel(), parent, entries)
+    rc = lib().csa_pages_fork(C.byref(cache), C.byref(pages), C.byref(window) if window is not None else None,
+                              _ptr(pending), int(child.numel()), _ptr(parent), _ptr(child), _ptr(entries),
+                              _ptr(ws), _nbytes(ws), _stream(stream))
+    _check(rc, "csa_pages_fork")
+
+
+def csa_pages_free(cache, pages, req, keep=None, ws=None, stream=None):
+    _same_length("csa_pages_free", req.numel(), keep)
+    rc = lib().csa_pages_free(C.byref(cache), C.byref(pages), int(req.numel()), _ptr(req), _ptr(keep), _ptr(ws),
+                              _nbytes(ws), _stream(stream))
+    _check(rc, "csa_pages_free")
+
+
+def csa_pages_compact(cache, pages, new_id, num_used, ws, stream=None):
+    rc = lib().csa_pages_compact(C.byref(cache), C.byref(pages), _ptr(new_id), _ptr(num_used), _ptr(ws),
+                                 _nbytes(ws), _stream(stream))
+    _check(rc, "csa_pages_compact")
+
+
 def csa_check_device_status(ws, stream=None):
     """Synchronises the stream; returns (status, flags) and clears the flags.
     ws=None reads the status word of csa_index_score_noalloc's fixed array."""
@@ -262,8 +322,8 @@ def csa_check_device_status(ws, stream=None):
 
 
 def csa_set_wait_budget(sm_clocks):
-    """Bound (in SM clocks) on each wait of the index score's pipeline; <= 0
-    restores the default.  Process-wide."""
+    """Bound (in SM clocks) on each wait of the index score's and the dense
+    attention's pipelines; <= 0 restores the default.  Process-wide."""
     _check(lib().csa_set_wait_budget(int(sm_clocks)), "csa_set_wait_budget")
 
 

@@ -227,6 +227,37 @@ csa_status_t append_args(const csa_cache_t* cache, const csa_window_t* window, c
   return CSA_OK;
 }
 
+// One reservation covers at most this many logical pages over all requests.
+constexpr int64_t kMaxReserveUnits = 1 << 26;
+
+// The arguments that every page call shares; no launch.
+csa_status_t pages_args(const csa_cache_t* cache, const csa_pages_t* pages, int32_t n, const int32_t* req,
+                        PagesArgs* out) {
+  const csa_status_t s = check_cache(cache);
+  if (s != CSA_OK) return s;
+  if (!pages || !pages->refs || !aligned(pages->refs, 16) || pages->page_table != cache->page_table)
+    return CSA_ERR_INVALID_ARGUMENT;
+  if (n < 0 || (n > 0 && (!req || !aligned(req, 4)))) return CSA_ERR_INVALID_ARGUMENT;
+  PagesArgs a{};
+  a.kv_pool = static_cast<uint8_t*>(cache->kv_pool);
+  a.idx_pool = static_cast<uint8_t*>(cache->idx_pool);
+  a.page_table = pages->page_table;
+  a.refs = pages->refs;
+  a.num_pages = cache->num_pages;
+  a.num_requests = cache->num_requests;
+  a.max_pages = cache->max_pages_per_req;
+  a.n = n;
+  a.req = req;
+  *out = a;
+  return CSA_OK;
+}
+
+// A workspace that holds the status word only, or none.
+csa_status_t check_status_ws(const void* ws, size_t ws_bytes) {
+  if (ws && (ws_bytes < kStatusBytes || !aligned(ws, 256))) return CSA_ERR_WORKSPACE_TOO_SMALL;
+  return CSA_OK;
+}
+
 csa_status_t check_decode(const csa_cache_t* cache, const csa_window_t* window, const csa_rows_t* rows,
                           int32_t n_idx_heads, const void* q_idx, const float* w, int32_t n_heads, const void* q,
                           const void* out, const void* ws, size_t ws_bytes) {
@@ -292,6 +323,15 @@ size_t csa_workspace_size(int32_t op, int32_t num_rows, int32_t max_entries, int
       return kStatusBytes + attn_tail_ws_bytes(num_rows, ws_heads(n_heads), num_sms());
     case CSA_OP_DECODE:
       return decode_layout(num_rows, max_entries, n_heads).end;
+    case CSA_OP_DENSE_ATTN:
+      return kStatusBytes + dense_ws_bytes(num_rows, max_entries, ws_heads(n_heads), num_sms());
+    case CSA_OP_PAGES_RESERVE:
+      return kStatusBytes + pages_reserve_ws_bytes(num_rows, max_entries);
+    case CSA_OP_PAGES_COMPACT:
+      return kStatusBytes + pages_compact_ws_bytes(num_rows);
+    case CSA_OP_PAGES_FORK:
+    case CSA_OP_PAGES_FREE:
+      return kStatusBytes;
     default:
       return 0;
   }
@@ -459,6 +499,119 @@ csa_status_t csa_step_ex(const csa_cache_t* cache, const csa_window_t* window, c
   // call's first kernel.
   return run_decode(cache, window, rows, n_idx_heads, q_idx, w, n_heads, q, softmax_scale, out, lse, topk_out, opts,
                     ws, ws_bytes, total_tokens > 0 ? Order::kChained : Order::kStream, stream);
+}
+
+csa_status_t csa_dense_attn(const csa_cache_t* cache, const csa_window_t* window, const csa_rows_t* rows,
+                            int32_t n_heads, const void* q, float softmax_scale, void* out, float* lse,
+                            const csa_opts_t* opts, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  csa_status_t s = check_cache(cache);
+  if (s != CSA_OK) return s;
+  if ((s = check_rows(rows, cache)) != CSA_OK) return s;
+  if ((s = check_window(window, rows->max_rows_per_req)) != CSA_OK) return s;
+  if (!attn_heads_supported(n_heads)) return CSA_ERR_UNSUPPORTED;
+  if ((s = check_attn_opts(opts, false)) != CSA_OK) return s;
+  if (opts && (opts->plan_out || opts->candidate_blocks)) return CSA_ERR_INVALID_ARGUMENT;
+  if (rows->num_rows == 0) return CSA_OK;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return CSA_ERR_INVALID_ARGUMENT;
+  const int sms = num_sms();
+  if (!ws || !aligned(ws, 256) ||
+      ws_bytes < kStatusBytes + dense_ws_bytes(rows->num_rows, rows->max_entries, n_heads, sms))
+    return CSA_ERR_WORKSPACE_TOO_SMALL;
+  DenseArgs a{};
+  a.kv_pool = static_cast<const uint8_t*>(cache->kv_pool);
+  a.page_table = cache->page_table;
+  a.num_pages = cache->num_pages;
+  a.num_requests = cache->num_requests;
+  a.max_pages = cache->max_pages_per_req;
+  a.P = cache->pool_ratio;
+  a.win_codes = window ? window->e4m3 : nullptr;
+  a.win_scale = window ? window->scale : nullptr;
+  a.win_cap = window ? window->capacity : 0;
+  a.row_req = rows->row_req;
+  a.row_pos = rows->row_pos;
+  a.num_rows = rows->num_rows;
+  a.H = n_heads;
+  a.max_entries = rows->max_entries;
+  a.max_rows_per_req = rows->max_rows_per_req;
+  a.q = static_cast<const uint16_t*>(q);
+  a.softmax_scale = softmax_scale;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.rope_cos = opts ? opts->rope_cos : nullptr;
+  a.rope_sin = opts ? opts->rope_sin : nullptr;
+  a.rope_rows = opts && opts->rope_cos ? opts->rope_rows : 0;
+  a.status = static_cast<uint32_t*>(ws);
+  a.wait_budget = g_wait_budget.load(std::memory_order_relaxed);
+  return from_cuda(launch_dense_attn(a, static_cast<uint8_t*>(ws) + kStatusBytes, sms, stream));
+}
+
+csa_status_t csa_pages_reserve(const csa_cache_t* cache, const csa_pages_t* pages, int32_t n, const int32_t* req,
+                               const int32_t* first, const int32_t* count, int32_t max_count, void* ws,
+                               size_t ws_bytes, cudaStream_t stream) {
+  PagesArgs a;
+  const csa_status_t s = pages_args(cache, pages, n, req, &a);
+  if (s != CSA_OK) return s;
+  if (max_count < 0) return CSA_ERR_INVALID_ARGUMENT;
+  if (n == 0) return CSA_OK;
+  if (!first || !count || !aligned(first, 4) || !aligned(count, 4)) return CSA_ERR_INVALID_ARGUMENT;
+  if (pages_reserve_units(n, max_count) > kMaxReserveUnits) return CSA_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, 256) || ws_bytes < kStatusBytes + pages_reserve_ws_bytes(n, max_count))
+    return CSA_ERR_WORKSPACE_TOO_SMALL;
+  a.arg0 = first;
+  a.arg1 = count;
+  a.max_count = max_count;
+  a.status = static_cast<uint32_t*>(ws);
+  a.ws = static_cast<uint8_t*>(ws) + kStatusBytes;
+  return from_cuda(launch_pages_reserve(a, num_sms(), stream));
+}
+
+csa_status_t csa_pages_fork(const csa_cache_t* cache, const csa_pages_t* pages, const csa_window_t* window,
+                            void* pending, int32_t n, const int32_t* parent, const int32_t* child,
+                            const int32_t* entries, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  PagesArgs a;
+  csa_status_t s = pages_args(cache, pages, n, child, &a);
+  if (s != CSA_OK) return s;
+  if ((s = check_window(window, 1)) != CSA_OK) return s;
+  if ((s = check_status_ws(ws, ws_bytes)) != CSA_OK) return s;
+  if (!aligned(pending, 16)) return CSA_ERR_INVALID_ARGUMENT;
+  if (n == 0) return CSA_OK;
+  if (!parent || !entries || !aligned(parent, 4) || !aligned(entries, 4)) return CSA_ERR_INVALID_ARGUMENT;
+  a.parent = parent;
+  a.arg0 = entries;
+  a.win_codes = window ? window->e4m3 : nullptr;
+  a.win_scale = window ? window->scale : nullptr;
+  a.win_cap = window ? window->capacity : 0;
+  a.pending = static_cast<uint16_t*>(pending);
+  a.status = static_cast<uint32_t*>(ws);
+  return from_cuda(launch_pages_fork(a, stream));
+}
+
+csa_status_t csa_pages_free(const csa_cache_t* cache, const csa_pages_t* pages, int32_t n, const int32_t* req,
+                            const int32_t* keep, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  PagesArgs a;
+  csa_status_t s = pages_args(cache, pages, n, req, &a);
+  if (s != CSA_OK) return s;
+  if ((s = check_status_ws(ws, ws_bytes)) != CSA_OK) return s;
+  if (!aligned(keep, 4)) return CSA_ERR_INVALID_ARGUMENT;
+  if (n == 0) return CSA_OK;
+  a.arg0 = keep;
+  a.status = static_cast<uint32_t*>(ws);
+  return from_cuda(launch_pages_free(a, stream));
+}
+
+csa_status_t csa_pages_compact(const csa_cache_t* cache, const csa_pages_t* pages, int32_t* new_id,
+                               int32_t* num_used, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  PagesArgs a;
+  const csa_status_t s = pages_args(cache, pages, 0, nullptr, &a);
+  if (s != CSA_OK) return s;
+  if (!aligned(new_id, 4) || !aligned(num_used, 4)) return CSA_ERR_INVALID_ARGUMENT;
+  if (!ws || !aligned(ws, 256) || ws_bytes < kStatusBytes + pages_compact_ws_bytes(cache->num_pages))
+    return CSA_ERR_WORKSPACE_TOO_SMALL;
+  a.new_id = new_id;
+  a.num_used = num_used;
+  a.status = static_cast<uint32_t*>(ws);
+  a.ws = static_cast<uint8_t*>(ws) + kStatusBytes;
+  return from_cuda(launch_pages_compact(a, num_sms(), stream));
 }
 
 csa_status_t csa_check_device_status(void* ws, cudaStream_t stream, uint32_t* flags_out) {

@@ -149,4 +149,62 @@ size_t attn_tail_ws_bytes(int32_t num_rows, int32_t H, int num_sms);
 // tail split.  The counters are zeroed before the call's first kernel.
 void attn_tail_setup(AttnArgs& a, void* base, size_t bytes, int num_sms);
 
+// Dense attention over every visible entry (csa_dense_attn).
+struct DenseArgs {
+  const uint8_t* kv_pool;
+  const int32_t* page_table;
+  int32_t num_pages, num_requests, max_pages, P;
+  const uint8_t* win_codes;            // null: no window
+  const float* win_scale;
+  int32_t win_cap;
+  const int32_t* row_req;
+  const int32_t* row_pos;
+  int32_t num_rows, H, max_entries, max_rows_per_req;
+  const uint16_t* q;                   // bf16 [R, H, 512]
+  float softmax_scale;
+  uint16_t* out;                       // bf16 [R, H, 512]
+  float* lse;                          // [R, H] or null
+  const float* rope_cos;               // [rope_rows, 32] or null
+  const float* rope_sin;
+  int32_t rope_rows;
+  uint32_t* status;
+  long long wait_budget;               // SM clocks a wait may take
+  // set by the launcher: the workspace past the status word
+  int4* rec;                           // [grid] a group cut at the CTA's end: first row, rows, first and last CTA
+  float* part;                         // [2 * grid][cols][512] unnormalised O
+  float* part_ml;                      // [2 * grid][2][cols] (m, l)
+};
+size_t dense_ws_bytes(int32_t num_rows, int32_t max_entries, int32_t H, int num_sms);
+cudaError_t launch_dense_attn(DenseArgs a, void* ws, int num_sms, cudaStream_t stream);
+
+// Page management (csa_pages_*).
+struct PagesArgs {
+  uint8_t* kv_pool;
+  uint8_t* idx_pool;
+  int32_t* page_table;
+  int32_t* refs;
+  int32_t num_pages, num_requests, max_pages;
+  int32_t n;                           // list length
+  const int32_t* req;                  // [n] requests (fork: the children)
+  const int32_t* parent;               // fork
+  const int32_t* arg0;                 // reserve: first; fork: entries; free: keep or null
+  const int32_t* arg1;                 // reserve: count
+  int32_t max_count;                   // reserve
+  uint8_t* win_codes;                  // fork
+  float* win_scale;
+  int32_t win_cap;
+  uint16_t* pending;
+  int32_t* new_id;                     // compact
+  int32_t* num_used;
+  uint32_t* status;
+  void* ws;
+};
+int64_t pages_reserve_units(int32_t n, int32_t max_count);
+size_t pages_reserve_ws_bytes(int32_t n, int32_t max_count);
+size_t pages_compact_ws_bytes(int32_t num_pages);
+cudaError_t launch_pages_reserve(const PagesArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_free(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesArgs& a, int num_sms, cudaStream_t stream);
+
 }  // namespace csa

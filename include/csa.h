@@ -119,6 +119,7 @@ typedef enum {
 #define CSA_FLAG_TOPK_OOB    0x4u   /* selected index outside the visible range */
 #define CSA_FLAG_TIMEOUT     0x8u   /* a bounded device wait ran out             */
 #define CSA_FLAG_APPEND      0x10u  /* token offsets inconsistent with total    */
+#define CSA_FLAG_NO_PAGES    0x20u  /* fewer free pages than a call needed      */
 
 /* Paged FP4 cache (caller-owned device memory). */
 typedef struct {
@@ -155,11 +156,17 @@ typedef struct {
  * CTA per SM are split over several CTAs that merge through the workspace
  * (see csa_sparse_attn); a workspace without that room (at least the size
  * computed for a device with num_rows or more SMs) runs every row whole.
+ * CSA_OP_DENSE_ATTN: also depends on the current device's SM count, and the
+ * call needs all of it.  The page calls: CSA_OP_PAGES_RESERVE takes the list
+ * length as num_rows and max_count as max_entries, CSA_OP_PAGES_COMPACT the
+ * pool's num_pages as num_rows, CSA_OP_PAGES_FORK and CSA_OP_PAGES_FREE none.
  * A workspace is zero-filled before its first use (its status word starts at
  * zero); the tail split's arrival counters are zeroed by each call that uses
  * them, so a workspace can serve calls of different shapes.  0 = bad op. */
 enum { CSA_OP_APPEND = 0, CSA_OP_INDEX_SCORE = 1, CSA_OP_TOPK = 2,
-       CSA_OP_SPARSE_ATTN = 3, CSA_OP_DECODE = 4 };
+       CSA_OP_SPARSE_ATTN = 3, CSA_OP_DECODE = 4, CSA_OP_DENSE_ATTN = 5,
+       CSA_OP_PAGES_RESERVE = 6, CSA_OP_PAGES_FORK = 7, CSA_OP_PAGES_FREE = 8,
+       CSA_OP_PAGES_COMPACT = 9 };
 CSA_API size_t csa_workspace_size(int32_t op, int32_t num_rows, int32_t max_entries, int32_t n_heads);
 
 /* csa_append -- pool, quantise and write new tokens ([SGL] "DSpark adaptation
@@ -402,6 +409,102 @@ CSA_API csa_status_t csa_step_ex(const csa_cache_t* cache, const csa_window_t* w
                                  void* out, float* lse, int32_t* topk_out, const csa_opts_t* opts,
                                  void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* csa_dense_attn -- for each row and head: softmax attention of q over EVERY
+ * visible FP4 main-KV entry (e < floor((t+1)/P), through the page table) and the
+ * FP8 window positions max(0,t-127)..t: csa_sparse_attn without a selection, for
+ * layers without an indexer, contexts the top 512 would cover anyway, and whole
+ * prompt chunks (rows of one request at consecutive positions, each seeing its
+ * own prefix).  K = V = the shared 512-d latent (MQA).
+ *  One work list of 128-key tiles over all rows is cut into equal shares, one
+ * per CTA; a row cut between CTAs leaves its partials in ws and a second kernel
+ * merges them by log-sum-exp, in a fixed order.
+ *  A row whose request or position is out of range, or which sees more entries
+ * than max_pages_per_req pages hold, raises CSA_FLAG_ROW_INVALID and gets a zero
+ * output and lse -inf, as does (without a flag) a row that sees nothing.  An
+ * entry whose page id is out of range is left out and raises CSA_FLAG_PAGE_OOB.
+ *  opts (nullable): rope_cos, rope_sin, rope_rows as csa_sparse_attn_ex; plans
+ * and candidate_blocks must be unset (CSA_ERR_INVALID_ARGUMENT).
+ *  Rounding: P is rounded once to fp16 (11 bits), as are rotated window values;
+ * rotated query values keep 22 bits, every other operand is exact, every sum and
+ * the softmax are fp32.  A query vector may have any magnitude (it is scaled by a power of two);
+ * window scales must stay below 2^15.
+ *  q bf16 [R, H, 512]; out bf16 [R, H, 512]; lse fp32 [R, H] (nullable, natural
+ * log).  n_heads 16, 32 or 64.  ws: csa_workspace_size(CSA_OP_DENSE_ATTN, R,
+ * max_entries, n_heads) bytes, 256-byte aligned.  out must not overlap any
+ * input. */
+CSA_API csa_status_t csa_dense_attn(const csa_cache_t* cache, const csa_window_t* window,
+                                    const csa_rows_t* rows, int32_t n_heads, const void* q,
+                                    float softmax_scale, void* out, float* lse, const csa_opts_t* opts,
+                                    void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Page management.  A pool's pages are counted by the table slots that name
+ * them: refs[p] slots (of all requests) hold page p, 0 means free; an empty slot
+ * is -1.  The calls below keep table and counts in step on the device, in stream
+ * order and without the host reading anything, so a step that reserves, appends
+ * and decodes can be captured in a graph.  A caller that holds a page outside
+ * the table (a prefix store) adds its own count.
+ *  Request lists are strictly increasing and padded at the end with -1; a list
+ * that is not, or an id past num_requests, raises CSA_FLAG_ROW_INVALID and the
+ * call changes nothing.  A table slot whose page id is past the pool, or whose
+ * page has no count, raises CSA_FLAG_PAGE_OOB; csa_pages_reserve leaves it as it
+ * is, the others empty it.  Results never depend on the order in which the
+ * device works. */
+typedef struct {
+  int32_t* page_table;             /* the cache's page_table, writable            */
+  int32_t* refs;                   /* [num_pages], 16-byte aligned                */
+} csa_pages_t;
+
+/* csa_pages_reserve -- makes entries first[i] .. first[i] + count[i] - 1 of
+ * request req[i] writable: each logical page among them that is empty gets a free
+ * page, and each that is shared (count > 1) is copied, both pools, to a free page
+ * that takes its place (copy on write; the old page's count drops by one, so if
+ * every holder copies in one call it becomes free).  Free pages are taken lowest
+ * id first, in list order and then page order; the pages that a call frees are
+ * not taken in it.  When they run out, the remaining pages are left as they were
+ * and CSA_FLAG_NO_PAGES is raised.  Call it before the csa_append of those
+ * entries.
+ *  req, first, count: [n] int32; max_count: host bound on count.  A request with
+ * first or count negative, count > max_count or pages past max_pages_per_req is
+ * left out and raises CSA_FLAG_ROW_INVALID.
+ *  ws: csa_workspace_size(CSA_OP_PAGES_RESERVE, n, max_count, 0) bytes, 256-byte
+ * aligned. */
+CSA_API csa_status_t csa_pages_reserve(const csa_cache_t* cache, const csa_pages_t* pages, int32_t n,
+                                       const int32_t* req, const int32_t* first, const int32_t* count,
+                                       int32_t max_count, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* csa_pages_fork -- request child[i] becomes a continuation of parent[i]: it
+ * releases the pages it held, then shares the parent's pages of entries 0 ..
+ * entries[i] - 1 (no page is copied: csa_pages_reserve does that when one of them
+ * writes), and the parent's window ring (window nullable) and pending token
+ * (nullable) are copied.  child is the request list; a parent may have several
+ * children, but none that is itself a child in the same call.  entries[i] < 0 or
+ * past max_pages_per_req pages leaves that child as it was and raises
+ * CSA_FLAG_ROW_INVALID.
+ *  ws: 256 bytes or more for the status word, 256-byte aligned, or NULL (faults
+ * are then not reported). */
+CSA_API csa_status_t csa_pages_fork(const csa_cache_t* cache, const csa_pages_t* pages, const csa_window_t* window,
+                                    void* pending, int32_t n, const int32_t* parent, const int32_t* child,
+                                    const int32_t* entries, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* csa_pages_free -- request req[i] keeps its first keep[i] entries (keep NULL:
+ * none) and releases every page past them.  keep[i] < 0 leaves the request as it
+ * was and raises CSA_FLAG_ROW_INVALID.  ws as csa_pages_fork. */
+CSA_API csa_status_t csa_pages_free(const csa_cache_t* cache, const csa_pages_t* pages, int32_t n,
+                                    const int32_t* req, const int32_t* keep, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream);
+
+/* csa_pages_compact -- moves pages so that the U used ones are pages 0 .. U - 1:
+ * the k-th lowest free id below U receives the k-th highest used page (both
+ * pools), and counts and the whole page table follow.  A page that stays is not
+ * touched; the bytes of a page left free are not changed.
+ *  new_id [num_pages] int32 (nullable): where each page went, -1 for free pages
+ * (to follow plans and pages held outside the table); num_used int32 [1]
+ * (nullable): U.
+ *  ws: csa_workspace_size(CSA_OP_PAGES_COMPACT, num_pages, 0, 0) bytes, 256-byte
+ * aligned. */
+CSA_API csa_status_t csa_pages_compact(const csa_cache_t* cache, const csa_pages_t* pages, int32_t* new_id,
+                                       int32_t* num_used, void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Synchronises `stream`, returns the status word's flags in *flags_out (host)
  * and clears it.  Returns CSA_OK, CSA_ERR_TIMEOUT or CSA_ERR_DEVICE_FAULT.
  * ws == NULL reads the status word of csa_index_score_noalloc's fixed scratch
@@ -409,14 +512,14 @@ CSA_API csa_status_t csa_step_ex(const csa_cache_t* cache, const csa_window_t* w
 CSA_API csa_status_t csa_check_device_status(void* ws, cudaStream_t stream, uint32_t* flags_out);
 
 /* csa_set_wait_budget -- failure detection (no counterpart in the pages).
- * Every wait of the index score's pipeline (a copy landing, an MMA
- * completing, a buffer coming free) is bounded by this many SM clocks; a wait
+ * Every wait of the index score's and the dense attention's pipelines (a copy
+ * landing, an MMA completing, a buffer coming free) is bounded by this many SM clocks; a wait
  * that runs out stops the kernel, which raises CSA_FLAG_TIMEOUT in the status
  * word, waits for the copies and tensor-core work it already issued, frees
  * its tensor memory and returns.  Process-wide; takes effect at the next
  * call's launch.  sm_clocks <= 0 restores the default (3e9 clocks, about 1.5
  * s).  A small budget is a way to exercise the time-out path without a
- * fault; scores are incomplete after a time-out. */
+ * fault; scores and outputs are incomplete after a time-out. */
 CSA_API csa_status_t csa_set_wait_budget(int64_t sm_clocks);
 
 CSA_API const char* csa_status_string(csa_status_t status);

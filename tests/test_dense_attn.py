@@ -1,0 +1,275 @@
+"""csa_dense_attn against attention in 64 bits over the cache's bytes: lengths
+from nothing to many tiles, every head count, groups of rows, windows, rotary
+tables, cut groups, extreme magnitudes, bad pages and rows; streams and graphs;
+and what the call refuses."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import fp4_sparse_attention_csa_gb300 as csa
+from dense_ref import Case
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    csa.build.build()
+    if torch.cuda.is_available():
+        torch.cuda.set_device(0)
+
+
+def rope_tables(rows, seed=5):
+    th = np.random.default_rng(seed).uniform(0, 2 * np.pi, (rows, 32))
+    return np.cos(th).astype(np.float32), np.sin(th).astype(np.float32)
+
+
+# ---- refusals (no kernel runs) --------------------------------------------------------
+def host_args(H=64):
+    buf = (C.c_uint8 * 65536)()
+    base = (C.addressof(buf) + 255) & ~255
+    pt, ints = (C.c_int32 * 4)(), (C.c_int32 * 8)()
+    cache = csa.CsaCache(base, base, C.addressof(pt), 1, 1, 1, 2)
+    rows = csa.CsaRows(1, C.addressof(ints), C.addressof(ints), 16, 1)
+    keep = (buf, pt, ints, cache, rows)
+    return keep, base, [C.byref(cache), None, C.byref(rows), H, base, 1.0, base, None, None, base, 1 << 40, None]
+
+
+def test_refusals_before_any_launch():
+    lib = csa.lib()
+    for at in (0, 2):
+        keep, base, args = host_args()
+        args[at] = None
+        assert lib.csa_dense_attn(*args) == 1, at
+    for at in (4, 6):                                     # q, out: missing, misaligned
+        for v in (None, "odd"):
+            keep, base, args = host_args()
+            args[at] = v and base + 2
+            assert lib.csa_dense_attn(*args) == 1, (at, v)
+    for H in (0, 8, 48, 63, 128, -16):
+        keep, base, args = host_args(H)
+        assert lib.csa_dense_attn(*args) == 2, H
+    for ws, n in ((None, 1 << 40), ("base", 256), ("odd", 1 << 40)):
+        keep, base, args = host_args()
+        args[9], args[10] = (None if ws is None else base + (16 if ws == "odd" else 0)), n
+        assert lib.csa_dense_attn(*args) == 3, (ws, n)
+    keep, base, args = host_args()
+    args[7] = base + 2                                    # lse misaligned
+    assert lib.csa_dense_attn(*args) == 1
+    for o in (csa.CsaOpts(base, None, None, None, 0, 0), csa.CsaOpts(None, base, None, None, 0, 0),
+              csa.CsaOpts(None, None, None, None, 0, 4), csa.CsaOpts(None, None, base, None, 4, 0),
+              csa.CsaOpts(None, None, base, base, 0, 0)):
+        keep, base, args = host_args()
+        args[8] = C.byref(o)
+        assert lib.csa_dense_attn(*args) == 1, (o.plan_in, o.plan_out, o.candidate_blocks, o.rope_rows)
+    keep, base, args = host_args()
+    win = csa.CsaWindow(base, base, 127)                  # a ring that cannot hold a row's window
+    args[1] = C.byref(win)
+    assert lib.csa_dense_attn(*args) == 1
+    keep, base, args = host_args()
+    none = csa.CsaRows(0, None, None, 0, 1)               # no rows: nothing to do
+    args[2] = C.byref(none)
+    assert lib.csa_dense_attn(*args) == 0
+
+
+def test_workspace_grows_with_the_call():
+    sizes = [csa.csa_workspace_size(csa.OP_DENSE_ATTN, *s) for s in ((1, 0, 16), (1, 100, 16), (4, 2000, 64))]
+    assert sizes[0] >= 256 and sizes == sorted(sizes)
+    assert csa.csa_workspace_size(csa.OP_DENSE_ATTN, -1, 0, 16) == 0
+
+
+# ---- numbers ----------------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("H", [16, 32, 64])
+@pytest.mark.parametrize("P,cap", [(1, 0), (1, 130), (2, 0), (2, 200)])
+def test_single_rows_of_every_length(H, P, cap):
+    """Positions around nothing, one entry, a page, a tile and several tiles."""
+    ctx = [1, 2, 3, 64 * P, 64 * P + 1, 127 * P, 128 * P, 129 * P - 1, 129 * P, 300 * P, 1000 * P + 1]
+    c = Case(1 + H + P + cap, ctx, P, cap)
+    req, pos = list(range(len(ctx))), [x - 1 for x in ctx]
+    q = c.queries(len(ctx), H)
+    assert c.run(csa, req, pos, H, q) == (0, 0)
+    c.check(req, pos, H, q)
+
+
+@gpu
+@pytest.mark.parametrize("H", [16, 32, 64])
+@pytest.mark.parametrize("cap,rope", [(0, False), (140, False), (140, True)])
+def test_verify_rows_share_their_request(H, cap, rope):
+    """Groups of 1 to 9 consecutive rows, whole and ragged, some from position 0."""
+    ctx, new = [9, 5, 700, 131, 1, 260], [9, 3, 7, 8, 1, 2]
+    c = Case(40 + H + cap, ctx, 2, cap)
+    req = [b for b in range(6) for _ in range(new[b])]
+    pos = [p for b in range(6) for p in range(ctx[b] - new[b], ctx[b])]
+    q = c.queries(len(req), H)
+    tab = rope_tables(700) if rope else None
+    assert c.run(csa, req, pos, H, q, rope=tab) == (0, 0)
+    c.check(req, pos, H, q, rope=tab)
+
+
+@gpu
+@pytest.mark.parametrize("H,P", [(16, 1), (32, 2), (64, 1)])
+def test_prompt_from_its_first_token(H, P):
+    """A whole prompt of odd length: each row sees its own prefix; with two
+    tokens per entry and no window the first row sees nothing."""
+    n = 333
+    c = Case(60 + H, [n, 77], P)
+    req, pos = [0] * n + [1] * 77, list(range(n)) + list(range(77))
+    q = c.queries(len(req), H)
+    assert c.run(csa, req, pos, H, q) == (0, 0)
+    c.check(req, pos, H, q, rows=list(range(0, n, 7)) + [0, 1, 2, 127, 128, 129, n - 1, n, n + 1, n + 76])
+
+
+@gpu
+@pytest.mark.parametrize("H,P,n", [(64, 2, 40001), (16, 1, 30000)])
+def test_one_long_row_is_cut_over_the_gpu(H, P, n):
+    c = Case(70 + H, [n], P, 128)
+    q = c.queries(1, H)
+    assert c.run(csa, [0], [n - 1], H, q) == (0, 0)
+    c.check([0], [n - 1], H, q)
+
+
+@gpu
+@pytest.mark.parametrize("H", [16, 64])
+def test_many_rows_of_mixed_lengths(H):
+    g = np.random.default_rng(3)
+    ctx = [int(x) for x in np.exp(g.uniform(np.log(2), np.log(6000), 211))]
+    c = Case(80 + H, ctx, 2, 128)
+    req, pos = list(range(211)), [x - 1 for x in ctx]
+    q = c.queries(211, H)
+    assert c.run(csa, req, pos, H, q) == (0, 0)
+    c.check(req, pos, H, q, rows=list(range(0, 211, 5)) + [210])
+
+
+@gpu
+def test_rows_in_any_order_and_gaps():
+    """Rows that skip positions, go back, repeat or leave requests out."""
+    c = Case(90, [900, 400, 50], 1, 300)
+    req, pos = [2, 2, 0, 0, 0, 0, 0, 1, 1, 0], [49, 48, 10, 11, 500, 500, 501, 399, 200, 899]
+    q = c.queries(len(req), 16)
+    assert c.run(csa, req, pos, 16, q) == (0, 0)
+    c.check(req, pos, 16, q)
+
+
+@gpu
+@pytest.mark.parametrize("qscale,scale", [(1e30, 1e-32), (1e-30, 1e28), (3e4, 2e-5), (1.0, 0.0), (1.0, -0.05)])
+def test_query_magnitudes_and_scales(qscale, scale):
+    c = Case(100, [500, 1500], 2, 128)
+    q = c.queries(2, 32, qscale)
+    q[0, 3] = 0.0
+    q[1, 5, 17] *= 256.0
+    assert c.run(csa, [0, 1], [499, 1499], 32, q, scale=scale) == (0, 0)
+    c.check([0, 1], [499, 1499], 32, q, scale=scale)
+
+
+@gpu
+def test_extreme_entries_and_window_scales():
+    """The largest and smallest codes and scales, window scales from 2^-40 to 2^10."""
+    c = Case(110, [640], 2, 128, spread=1.0)
+    page = c.table[0, 0]
+    c.kv[page, :8192] = 0x77                              # 6 everywhere
+    c.kv[page, 16384:17408] = 0x7E                        # times 448
+    c.kv[page, 17408:17920] = 0x01                        # times 2^-9
+    c.wscale[0] = np.exp2(np.linspace(-40, 10, 128)).astype(np.float32)
+    q = c.queries(1, 64, 0.01)
+    assert c.run(csa, [0], [639], 64, q) == (0, 0)
+    c.check([0], [639], 64, q)
+
+
+@gpu
+def test_the_running_max_grows_tile_by_tile():
+    """Ever larger logits along the cache move the max in every tile."""
+    c = Case(115, [2000], 1)
+    q = c.queries(1, 64)
+    n = 2000
+    sign = (q[0, 0] < 0).numpy().astype(np.uint8) * 8     # head 0 lines up with every entry
+    nib = 2 | sign
+    row = (nib[0::2] | (nib[1::2] << 4)).astype(np.uint8)
+    for e in range(n):
+        pg, s = c.table[0, e // 64], e % 64
+        c.kv[pg, 256 * s:256 * s + 256] = row
+        c.kv[pg, 16384 + 32 * s:16384 + 32 * s + 32] = 24 + (e * 40) // n
+    assert c.run(csa, [0], [n - 1], 64, q, scale=1.0) == (0, 0)
+    c.check([0], [n - 1], 64, q, scale=1.0)
+
+
+@gpu
+def test_nan_query_stays_in_its_column():
+    c = Case(120, [300], 2, 128)
+    q = c.queries(1, 16)
+    q[0, 2, 100] = float("nan")
+    assert c.run(csa, [0], [299], 16, q) == (0, 0)
+    out = c.out[0].float().cpu()
+    assert out[2].isnan().all() and c.lse[0, 2].isnan()
+    rest = [h for h in range(16) if h != 2]
+    assert not out[rest].isnan().any() and not c.lse[0, rest].isnan().any()
+
+
+# ---- faults that only the device sees ---------------------------------------------------
+@gpu
+def test_bad_pages_are_left_out_and_flagged():
+    c = Case(130, [1000, 600], 2, 128)
+    c.table[0, 2] = -1
+    c.table[1, 1] = c.num_pages
+    q = c.queries(2, 64)
+    assert c.run(csa, [0, 1], [999, 599], 64, q) == (5, csa.FLAG_PAGE_OOB)
+    c.check([0, 1], [999, 599], 64, q)
+
+
+@gpu
+def test_bad_rows_are_empty_and_flagged():
+    """Requests and positions out of range, more entries than the pages hold, a
+    position past the rotary tables; their neighbours are unaffected."""
+    c = Case(140, [300, 200], 1, 140)
+    held = c.table.shape[1] * 64
+    req, pos = [0, -1, 2, 0, 0, 1, 1], [299, 5, 5, -1, held, 150, 199]
+    tab = rope_tables(held + 8)
+    q = c.queries(len(req), 32)
+    assert c.run(csa, req, pos, 32, q, rope=tab, max_entries=300) == (5, csa.FLAG_ROW_INVALID)
+    c.check(req, pos, 32, q, rope=tab, rows=[0, 5, 6])
+    for r in (1, 2, 3, 4):
+        assert (c.out[r] == 0).all() and (c.lse[r] == -float("inf")).all()
+    short = rope_tables(180)
+    assert c.run(csa, [1, 1], [179, 180], 32, c.queries(2, 32), rope=short)[1] == csa.FLAG_ROW_INVALID
+    assert (c.out[1] == 0).all() and not (c.out[0] == 0).all()
+
+
+# ---- streams, graphs, repeats ------------------------------------------------------------
+@gpu
+def test_same_bits_again_without_lse_on_another_stream_and_from_a_graph():
+    g = np.random.default_rng(9)
+    ctx = [int(x) for x in g.integers(2, 4000, 40)]
+    c = Case(150, ctx, 2, 128)
+    req, pos = list(range(40)), [x - 1 for x in ctx]
+    q = c.queries(40, 64)
+    assert c.run(csa, req, pos, 64, q) == (0, 0)
+    first = c.out.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c.out.fill_(7.0)
+    s.wait_stream(torch.cuda.current_stream())
+    c.call(s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(c.out, first)
+    keep, c.lse = c.lse, None
+    c.out.fill_(7.0)
+    c.call()
+    assert torch.equal(c.out, first)
+    c.lse = keep
+    # two graphs that share the workspace, replayed in turn on new queries
+    graphs, outs = [], []
+    for k in range(2):
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            c.call(torch.cuda.current_stream())
+        graphs.append(gr)
+    other = c.queries(40, 64)
+    for k, data in ((0, other), (1, q), (0, other)):
+        c.d_q.copy_(data)
+        graphs[k].replay()
+        outs.append(c.out.clone())
+    assert csa.csa_check_device_status(c.ws) == (0, 0)
+    assert torch.equal(outs[1], first) and torch.equal(outs[0], outs[2]) and not torch.equal(outs[0], first)

@@ -70,7 +70,7 @@ def row_reference(kv_pool, table_row, num_pages, P, pos, q, scale, win=None, rop
         delta = delta + rotmag * (2.0 ** -22 + 2.0 ** -11 * rot.T)
     wt = p / l
     # P rounded to fp16: 2^-11, or half its smallest step (2^-25) where p is below
-    # 2^-14, relative to a running max that may lie 2^8 below the row's; then
+    # 2^-14, relative to a running max that may lie 2^14 below the row's; then
     # len/16 accumulations, the sums of p and the parts' merge.
     step = 2.0 ** -11 + (len(keys) / 16 + 96) * 2.0 ** -22
     A = np.abs(keys)

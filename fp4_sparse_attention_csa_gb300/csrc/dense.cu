@@ -4,8 +4,9 @@
 //
 // Mathematics.  A group is up to G = COLS / H rows of one request at consecutive
 // positions; its COLS = G * H columns are independent queries that share keys.
-// Its keys are one list: the W window tokens of the group's rows, then the n
-// entries that its last row sees; column c (row i) attends to the window
+// Its keys are one list: the W window tokens of the group's rows, padded to whole
+// tiles, then the n entries that its last row sees (so a tile of entries is two
+// whole pages, and finding its rows takes a few instructions); column c (row i) attends to the window
 // positions in [max(0, t_i - 127), t_i] and the entries below (t_i + 1) / P.
 // Per 128-key tile: S^T = K Q^T (M = 128 keys, N = COLS), p = 2^(s - m) with a
 // running max m per column, O^T += V^T P^T (M = 128 dims x 4, N = COLS); keys and
@@ -60,8 +61,8 @@ constexpr float kRescaleLog2 = 14.0f;
 // ---- the list of work ----------------------------------------------------------------
 struct Group {
   int r0, g, b, p0;                              // first row, rows, request, first position
-  int W, wlo;                                    // window keys and the first one's position
-  int keys, tiles;                               // tiles 0: the rows see nothing (or are invalid)
+  int W, Wp, wlo;                                // window keys, padded to tiles, and the first one's position
+  int n, tiles;                                  // tiles 0: the rows see nothing (or are invalid)
 };
 
 constexpr int kMaxPos = INT32_MAX - 1024;        // keys and positions stay within 32 bits
@@ -86,15 +87,17 @@ __device__ __forceinline__ Group group_at(const DenseArgs& a, int r, int G) {
   q.p0 = __ldg(a.row_pos + r);
   q.g = 1;
   if (!row_valid(a, q.b, q.p0)) {
-    q.W = q.wlo = q.keys = q.tiles = 0;
+    q.W = q.Wp = q.wlo = q.n = q.tiles = 0;
     return q;
   }
+#pragma unroll 1
   while (q.g < G && r + q.g < a.num_rows && row_continues(a, r + q.g)) ++q.g;
   const int last = q.p0 + q.g - 1;
   q.wlo = max(0, q.p0 - (WIN - 1));
   q.W = a.win_codes ? last - q.wlo + 1 : 0;
-  q.keys = q.W + entries_at(a, last);
-  q.tiles = (q.keys + kTileKeys - 1) / kTileKeys;
+  q.Wp = (q.W + kTileKeys - 1) / kTileKeys * kTileKeys;
+  q.n = entries_at(a, last);
+  q.tiles = (q.Wp + q.n + kTileKeys - 1) / kTileKeys;
   return q;
 }
 // A group of no tiles still takes one unit: its rows are written out empty.
@@ -137,6 +140,7 @@ __device__ __forceinline__ Share find_share(const DenseArgs& a, int G, ShareScra
   int run = -1;
   if (G > 1) {
     int start = -1;
+#pragma unroll 1
     for (int r = r_lo; r < r_hi; ++r)
       if (!row_continues(a, r)) start = r;
     const int upto = block_scan<true>(start, s.starts);
@@ -145,43 +149,44 @@ __device__ __forceinline__ Share find_share(const DenseArgs& a, int G, ShareScra
     __syncthreads();
     if (lane_id() == 0) run = tid > 0 ? s.run[warp_id() - 1] : -1;
   }
-  // visits the groups that begin in this thread's rows: f(row, units) until it is true
-  auto groups = [&](auto f) {
+  // twice over the groups that begin in this thread's rows: their units, then, in the
+  // one thread whose groups hold this share's first unit, the group that does
+  long long sum = 0, upto = 0, lo = 0, per = 0, units = 0, u = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
     int from = run;
+#pragma unroll 1
     for (int r = r_lo; r < r_hi; ++r) {
       if (G > 1 && row_continues(a, r)) {
         if ((r - from) % G != 0) continue;
       } else {
         from = r;
       }
-      if (f(r, group_units(group_at(a, r, G)))) break;
-    }
-  };
-  long long sum = 0;
-  groups([&](int, int n) {
-    sum += n;
-    return false;
-  });
-  const long long upto = block_scan<false>(sum, s.sums);
-  if (tid == kThreads - 1) s.total = upto;
-  __syncthreads();
-  const long long total = s.total, per = (total + gridDim.x - 1) / gridDim.x;
-  const long long lo = min(total, (long long)blockIdx.x * per), hi = min(total, lo + per);
-  long long u = upto - sum;
-  if (lo < hi && u <= lo && lo < upto) {         // exactly one thread
-    groups([&](int r, int n) {
-      if (lo >= u + n) {
+      const int n = group_units(group_at(a, r, G));
+      if (pass == 0) {
+        sum += n;
+      } else if (lo >= u + n) {
         u += n;
-        return false;
+      } else {
+        s.out.row = r;
+        s.out.t0 = (int)(lo - u);
+        break;
       }
-      s.out.row = r;
-      s.out.t0 = (int)(lo - u);
-      return true;
-    });
+    }
+    if (pass > 0) break;
+    upto = block_scan<false>(sum, s.sums);
+    if (tid == kThreads - 1) s.total = upto;
+    __syncthreads();
+    const long long total = s.total;
+    per = (total + gridDim.x - 1) / gridDim.x;
+    lo = min(total, (long long)blockIdx.x * per);
+    units = min(total, lo + per) - lo;
+    u = upto - sum;
+    if (units == 0 || lo < u || lo >= upto) break;
   }
   __syncthreads();
   Share h = s.out;
-  h.units = (int)(hi - lo);                      // a share is far below 2^31 tiles
+  h.units = (int)units;                          // a share is far below 2^31 tiles
   h.per = (int)per;
   return h;
 }
@@ -211,7 +216,7 @@ struct Smem {
   uint64_t k_full[2], k_free[2];                 // a chunk of K in tensor memory
   uint64_t v_full[4], v_free[4];                 // a 128-dim chunk of the tile in shared memory
   uint64_t s_full[2], s_free[2];                 // S^T of a tile
-  uint64_t p_full, p_free, q_full, o_full, o_free, drain;
+  uint64_t p_full, p_free, q_raw, q_full, q_free, o_full, o_free, drain;
   uint32_t moved[2];                             // bit c: column c's max moved
   uint32_t tmem_base;
   volatile int abort;                            // a wait ran out: every role leaves
@@ -357,7 +362,7 @@ struct Walk {
 // distinct banks; that permutes rows of O^T, and write_out undoes it.
 struct Raw {
   uint4 w[2][4];                                 // [chunk][row]
-  uint32_t sc[4];                                // [row]: the lane's quarter of the 16 scales of both chunks
+  uint16_t sc[2][4];                             // [chunk][row]: the lane's two scales
 };
 
 // Where the 4 dims from d (a multiple of 4) of a chunk sit: the 16-dim step of the
@@ -373,96 +378,42 @@ __device__ __forceinline__ uint32_t ldg_nc_u32(const void* p) {
   return v;
 }
 
-// A thread's four rows lie within 32 consecutive keys, so in one page or two
-// neighbouring ones.
-struct Pages {
-  int lo, hi;                                    // table words of the first row's page and the last row's
-};
-// e: the first row's entry; past the n entries, or a window key: -1.  Nothing looks
-// at the words until their bytes are fetched, a tile later.
-__device__ __forceinline__ Pages find_pages(const int32_t* row, int e, int n) {
-  Pages p{-1, -1};
-  if (e + 24 >= 0 && e < n) {
-    p.lo = __ldg(row + (max(e, 0) >> 6));
-    p.hi = __ldg(row + (min(e + 24, n - 1) >> 6));
-  }
-  return p;
-}
-// The page of row s, -1 when there is nothing to read (a page outside the pool
-// among them).
-__device__ __forceinline__ int page_of(const DenseArgs& a, const Pages& p, int e, int s, int n) {
-  const int x = e + 8 * s;
-  const int pg = (x >> 6) == (max(e, 0) >> 6) ? p.lo : p.hi;
-  return (x >= 0 && x < n && (uint32_t)pg < (uint32_t)a.num_pages) ? pg : -1;
-}
-
-// Row s's bytes of one chunk (h) or its scales.  A row with nothing to read takes
-// page 0's codes, and scales of zero.
-__device__ __forceinline__ const uint8_t* row_data(const DenseArgs& a, int pg, int slot, int chunk, int q) {
-  return a.kv_pool + (size_t)max(pg, 0) * KV_PAGE + slot * 256 + chunk * 64 + 16 * q;
-}
-__device__ __forceinline__ uint32_t row_scales(const DenseArgs& a, int pg, int slot, int wg, int q) {
-  return pg >= 0 ? ldg_nc_u32(a.kv_pool + (size_t)pg * KV_PAGE + KV_SCALE_OFF + slot * 32 + wg * 16 + 4 * q) : 0u;
-}
-// Where the thread's four rows of a tile of entries lie.
+// Where a warp's 32 entries lie: half a page.  A warp with nothing to read (past the
+// last entry, or a page outside the pool) takes some page's codes, and scales of zero.
 struct Rows {
-  const uint8_t* data[2];                        // row 0's bytes, were it in the first or the second page
-  const uint8_t* scales[2];
-  int slot0;
+  const uint8_t *data, *scales;                  // the lane's bytes of its first row
   uint32_t valid;                                // bit s: row s is there to read
-  __device__ __forceinline__ void set(const DenseArgs& a, const Pages& p, int e, int n, int wg, int q) {
-    slot0 = e & (PAGE - 1);
-    const bool ok[2] = {(uint32_t)p.lo < (uint32_t)a.num_pages, (uint32_t)p.hi < (uint32_t)a.num_pages};
-    valid = 0;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) valid |= (uint32_t)(e + 8 * s < n && ok[slot0 + 8 * s >= PAGE]) << s;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint8_t* page = a.kv_pool + (size_t)(ok[k] ? (k ? p.hi : p.lo) : 0) * KV_PAGE;
-      data[k] = page + (slot0 - k * PAGE) * 256 + wg * 128 + 16 * q;
-      scales[k] = page + KV_SCALE_OFF + (slot0 - k * PAGE) * 32 + wg * 16 + 4 * q;
-    }
+  // pg: the page table's word; e: the lane's first entry
+  __device__ __forceinline__ void set(const DenseArgs& a, int pg, int e, int n, int wg, int q) {
+    const bool ok = (uint32_t)pg < (uint32_t)a.num_pages;
+    const uint8_t* page = a.kv_pool + (size_t)(ok ? pg : 0) * KV_PAGE;
+    const int slot = e & (PAGE - 1);
+    data = page + slot * 256 + wg * 128 + 16 * q;
+    scales = page + KV_SCALE_OFF + slot * 32 + wg * 16 + 2 * q;
+    const int rows = ok ? min(4, max(0, (n - e + 7) >> 3)) : 0;
+    valid = (1u << rows) - 1u;
   }
-  // chunk h's bytes, and with the second the scales.  A row with nothing to read
-  // takes some page's codes, and scales of zero.
-  __device__ __forceinline__ void fetch(Raw& x, int h) const {
+  __device__ __forceinline__ void fetch(Raw& x) const {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int k = slot0 + 8 * s >= PAGE;
-      x.w[h][s] = ldg_nc_v4((k ? data[1] : data[0]) + s * 2048 + h * 64);
-      if (h == 1) {
-        x.sc[s] = 0u;
-        if ((valid >> s) & 1u) x.sc[s] = ldg_nc_u32((k ? scales[1] : scales[0]) + s * 256);
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        x.w[h][s] = ldg_nc_v4(data + s * 2048 + h * 64);
+        x.sc[h][s] = 0;
+        if ((valid >> s) & 1u) x.sc[h][s] = ldg_nc_u16(scales + s * 256 + h * 8);
       }
-    }
   }
 };
-// The lane's four scales, chunk 0's two in the low half, from its group's quarters.
-__device__ __forceinline__ uint32_t own_scales(uint32_t sc, int q) {
-  const uint32_t lo = __shfl_sync(0xFFFFFFFFu, sc, q >> 1, 4), hi = __shfl_sync(0xFFFFFFFFu, sc, 2 + (q >> 1), 4);
-  return __byte_perm(lo, hi, (q & 1) ? 0x7632 : 0x5410);
+// The page table's word for the warp's 32 entries from e0 on; -1 past the last one.
+__device__ __forceinline__ int find_page(const int32_t* row, int e0, int n) {
+  return e0 < n ? __ldg(row + (e0 >> 6)) : -1;
 }
 
 // h: tensor-memory register order of two rows (r, r + 8): pair k (two dims) of row j
 // of the thread's 16 pairs.
 __device__ __forceinline__ constexpr int h_at(int j, int k) { return 4 * (k / 2) + 2 * j + k % 2; }
 
-// The 16 pairs of an entry row's chunk; sc: its two scales.
-__device__ __forceinline__ void entry_to_f16(uint4 v, uint32_t sc, uint32_t (&o)[16]) {
-  const uint32_t sp = e4m3x2_to_f16((uint16_t)sc);
-  const __half2 hs0 = __low2half2(*reinterpret_cast<const __half2*>(&sp));
-  const __half2 hs1 = __high2half2(*reinterpret_cast<const __half2*>(&sp));
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t f[4];
-    e2m1x8_to_f16(w[i], f);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) o[4 * i + g] = hmul2_u32(f[g], i < 2 ? hs0 : hs1);
-  }
-}
-
-// Two words (16 dims, one scale, in both halves) of it.
+// Two words of an entry: 16 dims, one scale (in both halves).
 __device__ __forceinline__ void words_to_f16(uint32_t w0, uint32_t w1, __half2 scale, uint32_t (&o)[8]) {
   uint32_t f[4];
   e2m1x8_to_f16(w0, f);
@@ -524,73 +475,62 @@ struct Dequant {
   // second).  A window token is its codes times 2^e, e in [-14, 7] (exact); the rest
   // of its scale is mu.  ki: the thread's first key.
   __device__ __noinline__ static bool near_chunk(const DenseArgs& a, S& sm, bool values, int lane, int wg, int q,
-                                                 int key0, uint32_t tslot, int h, uint32_t tile, int ki, int W, int n,
-                                                 int wlo, int b, Pages p) {
-    const int c = 2 * wg + h, e = ki - W;
+                                                 int key0, uint32_t tslot, int h, uint32_t tile, int ki, int W,
+                                                 int wlo, int b) {
+    const int c = 2 * wg + h;
     const bool turn = c == 3 && q >= 2 && a.rope_cos != nullptr;
-    uint4 u[4], v[4];                            // 32 window codes, or an entry's 16 bytes in u
-    uint32_t sc[4];                              // a window token's scale, or an entry's scales
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      u[s] = v[s] = make_uint4(0u, 0u, 0u, 0u);
-      const int slot = (e + 8 * s) & (PAGE - 1), pg = page_of(a, p, e, s, n);
-      sc[s] = row_scales(a, pg, slot, wg, q);
-      if (ki + 8 * s < W) {
-        const size_t ring = (size_t)b * a.win_cap + (size_t)((wlo + ki + 8 * s) % a.win_cap);
-        const uint8_t* src = a.win_codes + ring * D + c * 128 + 32 * q;
-        u[s] = ldg_nc_v4(src);
-        v[s] = ldg_nc_v4(src + 16);
-        sc[s] = __float_as_uint(__ldg(a.win_scale + ring));
-      } else if (pg >= 0) {
-        u[s] = ldg_nc_v4(row_data(a, pg, slot, c, q));
-      }
-    }
-    auto row = [&](int s, uint32_t (&o)[16]) {
-      const uint32_t own = own_scales(sc[s], q) >> (16 * h);   // by all lanes
-      float mu = page_of(a, p, e, s, n) >= 0 ? 1.0f : -1.0f;
-      if (ki + 8 * s < W) {
-        const float ws = __uint_as_float(sc[s]);
-        const int ex = ws > 0.0f ? min(7, max(-14, (int)(__float_as_uint(ws) >> 23) - 127)) : -14;
-        const float pw = pow2(ex);
-        mu = ws * pow2(-ex);
-        const __half2 hp = __float2half2_rn(pw);
-        const uint32_t cw[8] = {u[s].x, u[s].y, u[s].z, u[s].w, v[s].x, v[s].y, v[s].z, v[s].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t f[2];
-          e4m3x4_to_f16(cw[i], f);
-          o[2 * i] = hmul2_u32(f[0], hp);
-          o[2 * i + 1] = hmul2_u32(f[1], hp);
-        }
-        if (turn) {                              // dims 448 + 32 (q - 2): the halves are q = 2 and 3
-          const int at = wlo + ki + 8 * s;
-          const size_t ring = (size_t)b * a.win_cap + (size_t)(at % a.win_cap);
-          const uint8_t* src = a.win_codes + ring * D + c * 128 + 32 * (5 - q);
-          uint32_t t[16];
-          rotate_window(a.rope_cos + (size_t)at * 32, a.rope_sin + (size_t)at * 32, q == 2, pw, u[s], v[s],
-                        ldg_nc_v4(src), ldg_nc_v4(src + 16), t);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = t[k];
-        }
-      } else {
-        entry_to_f16(u[s], own, o);
-      }
-      if (!values && c == 0 && q == 0) {
-        sm.mu[tile & 1][key0 + 8 * s] = mu;
-        if (mu < 0.0f && e + 8 * s < n) raise_flag(a.status, CSA_FLAG_PAGE_OOB);
-      }
-      __syncwarp();
-    };
     if (!values && c == 0 && lane == 0) sm.odd[tile & 1][key0 >> 5] = 1u;
     const bool ok = wait_or_abort(values ? &sm.v_free[c] : &sm.k_free[wg], values ? (tile & 1) ^ 1 : h ^ 1,
                                   a.wait_budget, &sm.abort);
     if (!__all_sync(0xFFFFFFFFu, ok)) return false;
     tc_fence_after();
+#pragma unroll 1
+    for (int s0 = 0; s0 < 4; s0 += 2) {          // two rows, r and r + 8
+      uint4 u[2], v[2], pu[2], pv[2];            // 32 codes, and the rotation's other half
+      float ws[2];
 #pragma unroll
-    for (int pair = 0; pair < 2; ++pair) {
+      for (int j = 0; j < 2; ++j) {
+        u[j] = v[j] = pu[j] = pv[j] = make_uint4(0u, 0u, 0u, 0u);
+        ws[j] = 0.0f;
+        const int k = ki + 8 * (s0 + j);
+        if (k < W) {
+          const size_t ring = (size_t)b * a.win_cap + (size_t)((wlo + k) % a.win_cap);
+          const uint8_t* src = a.win_codes + ring * D + c * 128 + 32 * q;
+          u[j] = ldg_nc_v4(src);
+          v[j] = ldg_nc_v4(src + 16);
+          if (turn) {                            // dims 448 + 32 (q - 2): the halves are q = 2 and 3
+            pu[j] = ldg_nc_v4(src + 32 * (5 - 2 * q));
+            pv[j] = ldg_nc_v4(src + 32 * (5 - 2 * q) + 16);
+          }
+          ws[j] = __ldg(a.win_scale + ring);
+        }
+      }
       uint32_t o[2][16];
-      row(2 * pair, o[0]);
-      row(2 * pair + 1, o[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int k = ki + 8 * (s0 + j);
+        const int ex = ws[j] > 0.0f ? min(7, max(-14, (int)(__float_as_uint(ws[j]) >> 23) - 127)) : -14;
+        const float pw = pow2(ex);
+        if (turn && k < W) {
+          const size_t at = (size_t)(wlo + k) * 32;
+          uint32_t t[16];
+          rotate_window(a.rope_cos + at, a.rope_sin + at, q == 2, pw, u[j], v[j], pu[j], pv[j], t);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[j][i] = t[i];
+        } else {
+          const __half2 hp = __float2half2_rn(pw);
+          const uint32_t cw[8] = {u[j].x, u[j].y, u[j].z, u[j].w, v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t f[2];
+            e4m3x4_to_f16(cw[i], f);
+            o[j][2 * i] = hmul2_u32(f[0], hp);
+            o[j][2 * i + 1] = hmul2_u32(f[1], hp);
+          }
+        }
+        if (!values && c == 0 && q == 0) sm.mu[tile & 1][key0 + 8 * (s0 + j)] = k < W ? ws[j] * pow2(-ex) : -1.0f;
+      }
+      __syncwarp();
       if (!values) {
         uint32_t t[32];
 #pragma unroll
@@ -598,13 +538,13 @@ struct Dequant {
           t[h_at(0, k)] = o[0][k];
           t[h_at(1, k)] = o[1][k];
         }
-        tmem_st_16x64(tslot + ((uint32_t)(16 * pair) << 16), t);
+        tmem_st_16x64(tslot + ((uint32_t)(8 * s0) << 16), t);
       } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(value_at(sm, c, key0, 2 * pair + j, q, i)) =
+            *reinterpret_cast<uint4*>(value_at(sm, c, key0, s0 + j, q, i)) =
                 make_uint4(o[j][4 * i], o[j][4 * i + 1], o[j][4 * i + 2], o[j][4 * i + 3]);
       }
     }
@@ -624,33 +564,30 @@ struct Dequant {
     uint32_t tile = 0;
     for (bool more = w.first(a, G, sh); more; more = w.next_segment(a, G)) {
       const int32_t* row = a.page_table + (size_t)w.gr.b * a.max_pages;
-      const int W = w.gr.W, n = w.gr.keys - W;
+      const int n = w.gr.n;
       int left = w.t_end - w.t;                  // tiles of the segment
       int ki = w.t * kTileKeys + key0;           // the thread's first key
 #pragma unroll 1
-      for (; left > 0 && ki - key0 < W; --left, ki += kTileKeys, ++tile) {
-        const Pages p = find_pages(row, ki - W, n);
+      for (; left > 0 && ki < w.gr.Wp; --left, ki += kTileKeys, ++tile) {
 #pragma unroll 1
         for (int part = 0; part < 4; ++part)     // both chunks for the first product, then for the second
-          if (!near_chunk(a, sm, part >= 2, lane, wg, q, key0, tslot, part & 1, tile, ki, W, n, w.gr.wlo, w.gr.b, p))
+          if (!near_chunk(a, sm, part >= 2, lane, wg, q, key0, tslot, part & 1, tile, ki, w.gr.W, w.gr.wlo, w.gr.b))
             return;
       }
       if (left <= 0) continue;
-      int e = ki - W;                            // the first row's entry
+      int e = ki - w.gr.Wp;                      // the thread's first entry
       Raw x;
       Rows at;
-      Pages next = find_pages(row, e, n);
-      at.set(a, next, e, n, wg, q);
-      at.fetch(x, 0);
-      at.fetch(x, 1);
+      at.set(a, find_page(row, e & ~31, n), e, n, wg, q);
+      at.fetch(x);
 #pragma unroll 1
       for (; left > 0; --left, ++tile) {
-        next = find_pages(row, e + kTileKeys, n);
+        int next = find_page(row, (e & ~31) + kTileKeys, n);
         if (wg == 0) {                           // keys past the last one and in bad pages are left out
           const bool odd = __any_sync(0xFFFFFFFFu, at.valid != 15u);
           if (lane == 0) sm.odd[tile & 1][key0 >> 5] = odd;
           if (odd && q == 0) {
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < 4; ++s) {
               const bool in = (at.valid >> s) & 1u;
               sm.mu[tile & 1][key0 + 8 * s] = in ? 1.0f : -1.0f;
@@ -658,86 +595,64 @@ struct Dequant {
             }
           }
         }
-        uint32_t sc[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) sc[s] = own_scales(x.sc[s], q);
         // ---- the first product's A operand: one chunk, whose values stay in registers,
         // then the other, which stays in the slot
-        if (!wait(&sm.k_free[wg], 1)) return;
-        tc_fence_after();
-        uint32_t t[2][32];
+        uint32_t t[4][16];                       // [2 pair + half]
 #pragma unroll
-        for (int pair = 0; pair < 2; ++pair) {
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(&sm.k_free[wg], h ^ 1)) return;
+          tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t o[16];
-            entry_to_f16(x.w[0][2 * pair + j], sc[2 * pair + j], o);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) t[pair][h_at(j, k)] = o[k];
-          }
-          tmem_st_16x64(tslot + ((uint32_t)(16 * pair) << 16), t[pair]);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&sm.k_full[wg], lane);
-        if (!wait(&sm.k_free[wg], 0)) return;
-        tc_fence_after();
-#pragma unroll
-        for (int pair = 0; pair < 2; ++pair) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) { // 32 columns: words 2 half and 2 half + 1 of two rows
+          for (int k = 0; k < 4; ++k) {          // 32 columns: words 2 half and 2 half + 1 of two rows
             uint32_t u[16];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint4 v = x.w[1][2 * pair + j];
-              const uint32_t sp = e4m3x2_to_f16((uint16_t)(sc[2 * pair + j] >> 16));
+              const uint4 v = x.w[h][2 * (k >> 1) + j];
+              const uint32_t sp = e4m3x2_to_f16(x.sc[h][2 * (k >> 1) + j]);
               const __half2 hs = *reinterpret_cast<const __half2*>(&sp);
               uint32_t o[8];
-              words_to_f16(half ? v.z : v.x, half ? v.w : v.y, half ? __high2half2(hs) : __low2half2(hs), o);
+              words_to_f16(k & 1 ? v.z : v.x, k & 1 ? v.w : v.y, k & 1 ? __high2half2(hs) : __low2half2(hs), o);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) u[h_at(j, k)] = o[k];
+              for (int i = 0; i < 8; ++i) u[h_at(j, i)] = o[i];
             }
-            tmem_st_16x32(tslot + ((uint32_t)(16 * pair) << 16) + 32 * half, u);
+            tmem_st_16x32(tslot + ((uint32_t)(16 * (k >> 1)) << 16) + 32 * (k & 1), u);
+            if (h == 0) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) t[k][i] = u[i];
+            }
           }
+          tmem_st_wait();
+          tc_fence_before();
+          warp_arrive(&sm.k_full[wg], lane);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&sm.k_full[wg], lane);
         // ---- the second product's, as the previous tile's chunks are used up; the next
         // tile's bytes are fetched meanwhile
         e += kTileKeys;
-        asm volatile("" : "+r"(next.lo), "+r"(next.hi));   // not looked at before here
+        asm volatile("" : "+r"(next));           // not looked at before here
         at.set(a, next, e, n, wg, q);            // past the last tile: nothing to read
-        if (!wait(&sm.v_free[2 * wg], (tile & 1) ^ 1)) return;
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(&sm.v_free[2 * wg + h], (tile & 1) ^ 1)) return;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t* r = t[s / 2] + h_at(s % 2, 4 * i);
-            *reinterpret_cast<uint4*>(value_at(sm, 2 * wg, key0, s, q, i)) = make_uint4(r[0], r[1], r[4], r[5]);
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int r = h_at(j, 4 * i);
+                *reinterpret_cast<uint4*>(value_at(sm, 2 * wg + h, key0, 2 * (k >> 1) + j, q, 2 * (k & 1) + i)) =
+                    make_uint4(t[k][r], t[k][r + 1], t[k][r + 4], t[k][r + 5]);
+              }
+          tc_fence_before();
+          fence_proxy_async_smem();
+          warp_arrive(&sm.v_full[2 * wg + h], lane);
+          if (h == 0) {
+            at.fetch(x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_ld_16x32(tslot + ((uint32_t)(16 * (k >> 1)) << 16) + 32 * (k & 1), t[k]);
+            tmem_ld_wait();
           }
-        fence_proxy_async_smem();
-        warp_arrive(&sm.v_full[2 * wg], lane);
-        at.fetch(x, 0);
-        at.fetch(x, 1);
-        uint32_t u[4][16];                       // [2 pair + half]
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld_16x32(tslot + ((uint32_t)(16 * (k >> 1)) << 16) + 32 * (k & 1), u[k]);
-        tmem_ld_wait();
-        if (!wait(&sm.v_free[2 * wg + 1], (tile & 1) ^ 1)) return;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int r = h_at(j, 4 * i);
-              *reinterpret_cast<uint4*>(value_at(sm, 2 * wg + 1, key0, 2 * (k >> 1) + j, q, 2 * (k & 1) + i)) =
-                  make_uint4(u[k][r], u[k][r + 1], u[k][r + 4], u[k][r + 5]);
-            }
-        tc_fence_before();
-        fence_proxy_async_smem();
-        warp_arrive(&sm.v_full[2 * wg + 1], lane);
+        }
       }
     }
   }
@@ -758,7 +673,7 @@ __device__ __forceinline__ void prefetch_tiles(const DenseArgs& a, Smem<COLS>& s
       if (c < w.gr.g * a.H) prefetch_l2(a.q + ((size_t)w.gr.r0 * a.H + c) * D, 8 * D * 2);
     }
     while (i - kAhead > sm.tile_now) __nanosleep(200);   // ends: S's issuer sets the last value on leaving
-    const int lo = max(0, w.t * kTileKeys - w.gr.W), hi = min(w.gr.keys, (w.t + 1) * kTileKeys) - w.gr.W;
+    const int lo = max(0, w.t * kTileKeys - w.gr.Wp), hi = min(w.gr.n, (w.t + 1) * kTileKeys - w.gr.Wp);
     const int page = (lo >> 6) + lane_id();
     if (lo < hi && page <= (hi - 1) >> 6) {
       const int pg = __ldg(a.page_table + (size_t)w.gr.b * a.max_pages + page);
@@ -797,21 +712,20 @@ struct Issue {
   }
   // step 0..3 of tile i's S: chunk (step / 2) of warpgroup (step % 2).  The step is a
   // constant, so that every operand's address is one.
-  template <int step>
-  __device__ __forceinline__ bool scores(uint32_t i) {
+  __device__ __forceinline__ bool scores(uint32_t i, int step, bool last) {
     if (!wait(&sm.k_full[step & 1], step >> 1)) return false;
     const uint64_t dQ = smem_desc(smem_u32(sm.q), 16, 1024, kSwizzle128B);
     const uint64_t dQl = smem_desc(smem_u32(sm.q_lo), 16, 1024, kSwizzle128B);
     constexpr uint32_t id = idesc_f16(128, COLS, 0, 0);
     const uint32_t ts = kTmemS + 64 * (i & 1), ta = kTmemK + 64 * (step & 1);
-    constexpr int c = 2 * (step & 1) + (step >> 1);
+    const int c = 2 * (step & 1) + (step >> 1);
     tc_fence_after();
     if (elect_one()) {
       const uint64_t dq = dQ + (uint64_t)(c * 2 * (COLS * 8));
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
         mma_f16_ts(ts, ta + 8 * ks, dq + (uint64_t)((ks >> 2) * (COLS * 8) + (ks & 3) * 2), id,
-                   (ks > 0 || step > 0) ? 1u : 0u);
+                   ks > 0 ? 1u : (uint32_t)(step > 0));
       if (step == 3 && a.rope_cos) {             // chunk 3 again, by the rotated dims' low parts
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
@@ -820,6 +734,7 @@ struct Issue {
       tc_commit(&sm.k_free[step & 1]);
       if (step == 3) {
         tc_commit(&sm.s_full[i & 1]);
+        if (last) tc_commit(&sm.q_free);         // of the segment
         mbar_arrive(&sm.s_full[i & 1]);          // orders the tile's mu before its softmax
       }
     }
@@ -827,13 +742,12 @@ struct Issue {
     return true;
   }
   // step 0..3 of a tile's O^T; first, last: of its segment
-  template <int step>
-  __device__ __forceinline__ bool values(uint32_t i, bool first, bool last) {
+  __device__ __forceinline__ bool values(uint32_t i, int step, bool first, bool last) {
     if (!wait(&sm.v_full[2 * (step & 1) + (step >> 1)], i & 1)) return false;
     const uint64_t dV = smem_desc(smem_u32(sm.k), 16384, 1024, kSwizzle128B);
     const uint64_t dP = smem_desc(smem_u32(sm.p), 8192, 1024, kSwizzle128B);
     constexpr uint32_t id = idesc_f16(128, COLS, 1, 1);
-    constexpr int c = 2 * (step & 1) + (step >> 1);
+    const int c = 2 * (step & 1) + (step >> 1);
     tc_fence_after();
     if (elect_one()) {
       const uint64_t dv = dV + (uint64_t)(c * 2048);
@@ -855,7 +769,10 @@ struct Issue {
     for (bool more = w.first(a, G, sh); more && w.settle(a, G); ++i, ++w.t) {
       if (w.t == w.t0 && !wait(&sm.q_full, seg++ & 1)) break;
       if (!wait(&sm.s_free[i & 1], ((i >> 1) & 1) ^ 1)) break;
-      if (!scores<0>(i) || !scores<1>(i) || !scores<2>(i) || !scores<3>(i)) break;
+      bool ok = true;
+#pragma unroll 1
+      for (int step = 0; step < 4 && ok; ++step) ok = scores(i, step, w.t + 1 == w.t_end);
+      if (!ok) break;
       if (lane_id() == 0) sm.tile_now = (int)i;
     }
     if (lane_id() == 0) sm.tile_now = INT32_MAX;   // lets the prefetching warp go
@@ -867,33 +784,64 @@ struct Issue {
       const bool first = w.t == w.t0, last = w.t + 1 == w.t_end;
       if (!wait(&sm.p_full, i & 1)) break;
       if (first && !wait(&sm.o_free, (seg++ & 1) ^ 1)) break;
-      if (!values<0>(i, first, last) || !values<1>(i, first, last) || !values<2>(i, first, last) ||
-          !values<3>(i, first, last))
-        break;
+      bool ok = true;
+#pragma unroll 1
+      for (int step = 0; step < 4 && ok; ++step) ok = values(i, step, first, last);
+      if (!ok) break;
     }
   }
 };
 
+__device__ __forceinline__ void swap2(uint2& a, uint2& b) {
+  const uint2 t = a;
+  a = b;
+  b = t;
+}
 // ---- queries ------------------------------------------------------------------------------
-// Columns c0 .. c0 + n - 1, of one row, to shared memory, fp16, by one warp: N at a
-// time, the next N in flight meanwhile.
-template <int COLS, int N>
-__device__ __forceinline__ void load_queries(const DenseArgs& a, Smem<COLS>& sm, const Group& gr, int c0, int n) {
-  const int lane = lane_id();
-  const bool in = c0 < gr.g * a.H, rope = a.rope_cos != nullptr && in;
-  const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)gr.r0 * a.H + c0) * D) + 2 * lane;
-  uint4 raw[N][2];
-  float cs[16], sn[16];
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    raw[j][0] = raw[j][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (in) {
-      raw[j][0] = __ldg(src + j * (D / 8));
-      raw[j][1] = __ldg(src + j * (D / 8) + 1);
+// One warp copies the next segment's bf16 queries to Q's place as soon as the last S
+// of the segment before is complete, while that segment's last softmax and O^T run.
+// Column c's 128-byte piece of an atom lies where the fp16 ones will; pieces of 16
+// bytes swap places in odd atoms, so that the warp that converts a column reads
+// without bank conflicts.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t bytes) {   // the rest is zero
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+template <int COLS>
+__device__ __forceinline__ void fetch_queries(const DenseArgs& a, Smem<COLS>& sm, const Share& sh, int G) {
+  Walk w;
+  uint32_t seg = 0;
+#pragma unroll 1
+  for (bool more = w.first(a, G, sh); more; more = w.next_segment(a, G)) {
+    if (w.t >= w.t_end) continue;
+    if (seg > 0) {
+      const bool ok = wait_or_abort(&sm.q_free, (seg - 1) & 1, a.wait_budget, &sm.abort);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
     }
+    const int cols = w.gr.g * a.H;
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(a.q + (size_t)w.gr.r0 * a.H * D);
+#pragma unroll 8
+    for (int k = lane_id(); k < COLS * 64; k += 32) {
+      const int c = k >> 6, atom = (k >> 3) & 7;
+      const bool in = c < cols;
+      cp_async16(sm.q + atom * (COLS * 128) + c * 128 + 16 * ((k & 7) ^ (atom & 1)), src + (in ? 16 * k : 0),
+                 in ? 16u : 0u);
+    }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.q_raw)) : "memory");
+    ++seg;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// A softmax warp's quarter of the columns to fp16, in place: a column's 512 dims are
+// one warp's, 16 consecutive ones a lane, and are all read before any is written.
+template <int COLS>
+__device__ __forceinline__ void convert_queries(const DenseArgs& a, Smem<COLS>& sm, const Group& gr, int warp, int lane) {
+  constexpr int N = 2;                           // columns at a time
+  const int c_lo = warp * (COLS / 4);
+  const bool rope = a.rope_cos != nullptr && c_lo < gr.g * a.H;
+  float cs[16], sn[16];
   if (rope && lane >= 28) {                      // the row's table entries of this lane's 16 dims
-    const size_t at = (size_t)(gr.p0 + c0 / a.H) * 32 + 16 * (lane & 1);
+    const size_t at = (size_t)(gr.p0 + c_lo / a.H) * 32 + 16 * (lane & 1);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       cs[i] = __ldg(a.rope_cos + at + i);
@@ -901,23 +849,18 @@ __device__ __forceinline__ void load_queries(const DenseArgs& a, Smem<COLS>& sm,
     }
   }
 #pragma unroll 1
-  for (int done = 0; done < n; done += N) {
+  for (int c = c_lo; c < c_lo + COLS / 4; c += N) {
     float f[N][16];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const uint32_t w[8] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w,
-                             raw[j][1].x, raw[j][1].y, raw[j][1].z, raw[j][1].w};
+      const uint8_t* src = sm.q + (lane >> 2) * (COLS * 128) + (c + j) * 128 + 32 * (lane & 3);
+      const uint4 r0 = *reinterpret_cast<const uint4*>(src + 16 * ((lane >> 2) & 1));
+      const uint4 r1 = *reinterpret_cast<const uint4*>(src + 16 * (((lane >> 2) & 1) ^ 1));
+      const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         f[j][2 * i] = __uint_as_float(w[i] << 16);
         f[j][2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
-    if (in && done + N < n) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        raw[j][0] = __ldg(src + (done + N + j) * (D / 8));
-        raw[j][1] = __ldg(src + (done + N + j) * (D / 8) + 1);
       }
     }
     if (rope) {                                  // dims 448.. are lanes 28, 29 and 30, 31
@@ -940,105 +883,92 @@ __device__ __forceinline__ void load_queries(const DenseArgs& a, Smem<COLS>& sm,
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) big[j] = warp_top(big[j]);
+    __syncwarp();                                // both columns have been read
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int c = c0 + done + j;
-      // 2^-e puts the largest magnitude in [128, 256); in two factors, as 2^-e may be
-      // past the fp32 range
-      const int ex = max(1, (int)(__float_as_uint(big[j]) >> 23));
-      const int e = (big[j] > 0.0f && ex < 255) ? ex - 127 - 7 : 0, e1 = e / 2, e2 = e - e1;
-      if (lane == 0) sm.factor[c] = a.softmax_scale * kLog2e * pow2(e1) * pow2(e2);
-      const float s1 = pow2(-e1), s2 = pow2(-e2);
-      const int row = (c >> 3) * 1024;
+      // 2^-e puts the largest magnitude in [128, 256); e >= -126 keeps it in fp32's
+      // range, and a query of such small elements has no logit to speak of
+      const int ex = (int)(__float_as_uint(big[j]) >> 23);
+      const int e = (ex > 0 && ex < 255) ? max(ex - 127 - 7, -126) : 0;
+      if (lane == 0) sm.factor[c + j] = a.softmax_scale * kLog2e * pow2(e);
+      const float s1 = pow2(-e);
+      uint2 hi[4], lo[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {              // 4 dims at a time
-        const float x0 = f[j][4 * u] * s1 * s2, x1 = f[j][4 * u + 1] * s1 * s2;
-        const float x2 = f[j][4 * u + 2] * s1 * s2, x3 = f[j][4 * u + 3] * s1 * s2;
+        const float x0 = f[j][4 * u] * s1, x1 = f[j][4 * u + 1] * s1;
+        const float x2 = f[j][4 * u + 2] * s1, x3 = f[j][4 * u + 3] * s1;
         const __half2 h0 = __floats2half2_rn(x0, x1), h1 = __floats2half2_rn(x2, x3);
-        int stp, place;
-        q_place(16 * (lane & 7) + 4 * u, stp, place);
-        const uint32_t at = row + swz128(c & 7, 2 * (stp & 3) + (place >> 1)) + 8 * (place & 1);
-        uint2 v;
-        v.x = *reinterpret_cast<const uint32_t*>(&h0);
-        v.y = *reinterpret_cast<const uint32_t*>(&h1);
-        *reinterpret_cast<uint2*>(sm.q + (2 * (lane >> 3) + (stp >> 2)) * (COLS * 128) + at) = v;
-        if (rope && lane >= 28) {
+        hi[u].x = *reinterpret_cast<const uint32_t*>(&h0);
+        hi[u].y = *reinterpret_cast<const uint32_t*>(&h1);
+        if (rope) {
           const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
           const __half2 l0 = __floats2half2_rn(x0 - f0.x, x1 - f0.y), l1 = __floats2half2_rn(x2 - f1.x, x3 - f1.y);
-          v.x = *reinterpret_cast<const uint32_t*>(&l0);
-          v.y = *reinterpret_cast<const uint32_t*>(&l1);
-          *reinterpret_cast<uint2*>(sm.q_lo + (stp >> 2) * (COLS * 128) + at) = v;
+          lo[u].x = *reinterpret_cast<const uint32_t*>(&l0);
+          lo[u].y = *reinterpret_cast<const uint32_t*>(&l1);
         }
+      }
+      // lanes of different atoms begin with different steps: their banks differ
+      const int first = (lane & 1) | ((lane >> 2) & 2);
+#pragma unroll
+      for (int u = 0; u < 4; u += 2)
+        if (first & 1) swap2(hi[u], hi[u + 1]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (first & 2) swap2(hi[u], hi[u + 2]);
+      const int place = (lane >> 1) & 3;         // as q_place has it for dims 16 (lane % 8) + 4 u; step 4 (lane % 2) + u
+      uint8_t* dst = sm.q + (2 * (lane >> 3) + (lane & 1)) * (COLS * 128) + ((c + j) >> 3) * 1024 + 8 * (place & 1);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<uint2*>(dst + swz128((c + j) & 7, 2 * (u ^ first) + (place >> 1))) = hi[u];
+      if (rope && lane >= 28) {
+        uint8_t* low = sm.q_lo + (lane & 1) * (COLS * 128) + ((c + j) >> 3) * 1024 + 8 * (place & 1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<uint2*>(low + swz128((c + j) & 7, 2 * u + (place >> 1))) = lo[u];
       }
     }
   }
 }
 
 // ---- output -------------------------------------------------------------------------------
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // O^T of a segment to its rows (kParts: to a part), by the softmax warps.  Each lane
-// holds a dim: the columns are put together in P's place, which no product uses now,
-// and leave as one bulk copy each.
+// holds a dim of 16 columns at a time, so a store of a column is one run of 32 dims;
+// neighbours swap halves of two columns to store pairs of bf16.  (Put together in
+// shared memory and sent as bulk copies, 64 columns took 19000 clocks, most of them
+// waiting for the copies to read.)
 template <int COLS, bool kParts>
 __device__ __forceinline__ void write_out(const DenseArgs& a, Smem<COLS>& sm, int warp, int lane, int r0, int cols,
                                           int slot) {
-  constexpr int kRound = kParts ? 8 : 16;        // columns put together at a time
-  constexpr int kElem = kParts ? 4 : 2, kRow = D * kElem;
   const int d = 32 * warp + (lane ^ (8 * (warp & 2)));   // the lane's dim in a chunk, as the tile was laid out
 #pragma unroll 1
-  for (int c0 = 0; c0 < cols; c0 += kRound) {
-    if (c0 > 0) {                                // the round before has been read
-      if (warp == 0) bulk_wait_read();
-      softmax_sync();
-    }
+  for (int j = 0; j < cols / 8; ++j) {           // 16 columns of two chunks
+    const int c0 = 16 * (j >> 1), dc = 2 * (j & 1);
+    const uint32_t ta = 64 * dc + ((uint32_t)(32 * warp) << 16) + c0;
+    uint32_t v[2][16];
+    tmem_ld16(ta, v[0]);
+    tmem_ld16(ta + 64, v[1]);
+    tmem_ld_wait();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {       // two chunks at a time
-      uint32_t v[2][kRound];
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t ta = 64 * (2 * half + j) + ((uint32_t)(32 * warp) << 16) + c0;
-        if constexpr (kParts) {
+      for (int k = 0; k < 16; ++k) asm volatile("" : "+r"(v[h][k]));   // not before the wait
+      if constexpr (kParts) {
+        float* dst = a.part + ((size_t)slot * COLS + c0) * D + 128 * (dc + h) + d;
 #pragma unroll
-          for (int k = 0; k < kRound; k += 4) {
-            uint32_t u[4];
-            tmem_ld4(ta + k, u);
+        for (int k = 0; k < 16; ++k) dst[k * D] = __uint_as_float(v[h][k]);
+      } else {
+        // the even lane of a pair stores column k, the odd one column k + 1
+        const int odd = lane & 1;
+        uint16_t* dst = a.out + ((size_t)r0 * a.H + c0 + odd) * D + 128 * (dc + h) + (d & ~1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[j][k + i] = u[i];
-          }
-        } else {
-          tmem_ld16(ta, v[j]);
+        for (int k = 0; k < 16; k += 2) {
+          const float x0 = __uint_as_float(v[h][k]) * sm.corr[c0 + k];
+          const float x1 = __uint_as_float(v[h][k + 1]) * sm.corr[c0 + k + 1];
+          const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? x0 : x1, 1);
+          const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(got, x1) : __floats2bfloat162_rn(x0, got);
+          *reinterpret_cast<__nv_bfloat162*>(dst + k * D) = o;
         }
       }
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint8_t* dst = sm.p + kElem * (128 * (2 * half + j) + d);
-#pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-          asm volatile("" : "+r"(v[j][k]));      // not before the wait
-          if constexpr (kParts) {
-            *reinterpret_cast<uint32_t*>(dst + k * kRow) = v[j][k];
-          } else {
-            const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[j][k]) * sm.corr[c0 + k]);
-            *reinterpret_cast<uint16_t*>(dst + k * kRow) = *reinterpret_cast<const uint16_t*>(&o);
-          }
-        }
-      }
-    }
-    fence_proxy_async_smem();
-    softmax_sync();
-    if (warp == 0 && lane < kRound) {
-      uint8_t* to = kParts ? reinterpret_cast<uint8_t*>(a.part + ((size_t)slot * COLS + c0 + lane) * D)
-                           : reinterpret_cast<uint8_t*>(a.out + ((size_t)r0 * a.H + c0 + lane) * D);
-      bulk_store(to, sm.p + lane * kRow, kRow);
-      bulk_commit();
     }
   }
 }
@@ -1047,7 +977,6 @@ __device__ __forceinline__ void write_out(const DenseArgs& a, Smem<COLS>& sm, in
 template <int COLS>
 struct Softmax {
   using S = Smem<COLS>;
-  static constexpr int HB = COLS < 32 ? COLS : 32, NB = COLS / HB;   // columns reduced at a time
   const DenseArgs& a;
   S& sm;
   int lane, warp;                                // warp 0..3: 32 keys, and 32 dims of each chunk
@@ -1067,49 +996,48 @@ struct Softmax {
   }
   __device__ __forceinline__ bool run(const Share& sh, int G, int4& rec) {
     Walk w;
-    uint32_t i = 0, outs = 0;
+    uint32_t i = 0, outs = 0, segs = 0;
     int prev_r0 = -1, prev_cols = 0, prev_slot = 0;
     const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
     const int mykey = 32 * warp + lane, tid = mykey;
-    constexpr int kShift = RedShift<HB>::v;
-    // the previous segment's output, once its last O^T is complete
-    auto flush = [&]() -> bool {
-      if (prev_r0 < 0) return true;
-      const bool ok = wait(&sm.o_full, outs & 1);
-      if (softmax_sync_or(!ok)) return false;
-      ++outs;
-      tc_fence_after();
-      if (prev_slot < 0) write_out<COLS, false>(a, sm, warp, lane, prev_r0, prev_cols, 0);
-      else write_out<COLS, true>(a, sm, warp, lane, prev_r0, prev_cols, prev_slot);
-      if (warp == 0) bulk_wait_read();           // P may be written again
-      softmax_sync();
-      tc_fence_before();
-      warp_arrive(&sm.o_free, lane);
-      prev_r0 = -1;
-      return true;
-    };
-    for (bool more = w.first(a, G, sh); more; more = w.next_segment(a, G)) {
-      const int cols = w.gr.g * a.H;
+    bool more = w.first(a, G, sh);
+#pragma unroll 1
+    for (;; more = w.next_segment(a, G)) {
+      const int cols = more ? w.gr.g * a.H : 0;
       const bool whole = w.whole();
       const int slot = whole ? -1 : (w.t0 > 0 ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1);
-      if (!whole && w.t0 == 0)
+      if (more && !whole && w.t0 == 0)
         rec = make_int4(w.gr.r0, w.gr.g, blockIdx.x, blockIdx.x + (group_units(w.gr) - w.left + sh.per - 1) / sh.per);
-      if (w.t >= w.t_end) {                      // rows that see nothing
+      if (more && w.t >= w.t_end) {              // rows that see nothing
         if (!row_valid(a, w.gr.b, w.gr.p0) && tid == 0) raise_flag(a.status, CSA_FLAG_ROW_INVALID);
         uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)w.gr.r0 * a.H * D);
         for (int k = tid; k < cols * (D / 8); k += 32 * kSoftmaxWarps) dst[k] = make_uint4(0u, 0u, 0u, 0u);
         if (a.lse && tid < cols) a.lse[(size_t)w.gr.r0 * a.H + tid] = -INFINITY;
         continue;
       }
-      if (i > 0) load_queries<COLS, 4>(a, sm, w.gr, warp * (COLS / 4), COLS / 4);   // a quarter of the columns
-      if (tid < COLS) sm.neg_m[tid] = 0.0f;
-      fence_proxy_async_smem();
-      warp_arrive(&sm.q_full, lane);
-      softmax_sync();                            // factors and maxima visible to all softmax warps
-      if (!flush()) return false;
+      if (more) {
+        (void)wait(&sm.q_raw, segs++ & 1);       // one that runs out ends the role at S's wait
+        convert_queries<COLS>(a, sm, w.gr, warp, lane);
+        if (tid < COLS) sm.neg_m[tid] = 0.0f;
+        fence_proxy_async_smem();
+        warp_arrive(&sm.q_full, lane);
+        softmax_sync();                          // factors and maxima visible to all softmax warps
+      }
+      if (prev_r0 >= 0) {                        // the segment before, once its last O^T is complete
+        const bool ok = wait(&sm.o_full, outs & 1);
+        if (softmax_sync_or(!ok)) return false;
+        ++outs;
+        tc_fence_after();
+        if (prev_slot < 0) write_out<COLS, false>(a, sm, warp, lane, prev_r0, prev_cols, 0);
+        else write_out<COLS, true>(a, sm, warp, lane, prev_r0, prev_cols, prev_slot);
+        tc_fence_before();
+        warp_arrive(&sm.o_free, lane);
+        prev_r0 = -1;
+      }
+      if (!more) break;
       bool fresh = true;                         // no key of the segment seen yet: neg_m is not a max
       // keys that every column sees (window keys aside); none when columns are unused
-      const int all_see = cols == COLS ? w.gr.W + entries_at(a, w.gr.p0) : 0;
+      const int all_see = cols == COLS ? w.gr.Wp + entries_at(a, w.gr.p0) : 0;
       float2 lpart[COLS / 2];                    // this key's share of the columns' sums of p
 #pragma unroll
       for (int k = 0; k < COLS / 2; ++k) lpart[k] = make_float2(0.0f, 0.0f);
@@ -1128,61 +1056,81 @@ struct Softmax {
           if (sm.odd[i & 1][warp]) mu = sm.mu[i & 1][mykey];
           int ilo = 0, ihi = -1;                 // rows of the group
           if (mu >= 0.0f) {
-            if (ki < w.gr.W) {
+            if (ki < w.gr.Wp) {
               ilo = max(0, w.gr.wlo + ki - w.gr.p0);
               ihi = min(w.gr.g - 1, w.gr.wlo + ki + (WIN - 1) - w.gr.p0);
             } else {
-              ilo = max(0, ((ki - w.gr.W + 1) << (a.P - 1)) - 1 - w.gr.p0);
+              ilo = max(0, ((ki - w.gr.Wp + 1) << (a.P - 1)) - 1 - w.gr.p0);
               ihi = w.gr.g - 1;
             }
           }
           clo = ilo * a.H;
           chi = (ihi + 1) * a.H;
         }
-        // x = logit - m; a column that does not see the key: -inf
-        float2 x[COLS / 2];
-#pragma unroll
-        for (int k = 0; k < COLS; k += 16) tmem_ld16_pairs(ts + k, &x[k / 2]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < COLS / 2; ++k) asm volatile("" : "+f"(x[k].x), "+f"(x[k].y));   // not before the wait
-        tc_fence_before();
-        warp_arrive(&sm.s_free[i & 1], lane);
         const float4* fac = reinterpret_cast<const float4*>(sm.factor);
         const float4* mr = reinterpret_cast<const float4*>(sm.neg_m);
-        if (!plain) {
+        const float4* al = reinterpret_cast<const float4*>(sm.corr);
+        float2 x[COLS / 2];
+        bool moved = false;
+#pragma unroll 1
+        for (;;) {                               // again once the running max has moved
+          // x = logit - m; a column that does not see the key: -inf
 #pragma unroll
-          for (int k = 0; k < COLS / 2; ++k) x[k] = make_float2(x[k].x * mu, x[k].y * mu);
-        }
+          for (int k = 0; k < COLS; k += 16) tmem_ld16_pairs(ts + k, &x[k / 2]);
+          tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < COLS; k += 4) {
-          const float4 f = fac[k / 4], m = mr[k / 4];
-          x[k / 2] = fma2(x[k / 2], make_float2(f.x, f.y), make_float2(m.x, m.y));
-          x[k / 2 + 1] = fma2(x[k / 2 + 1], make_float2(f.z, f.w), make_float2(m.z, m.w));
-        }
-        if (!plain) {
+          for (int k = 0; k < COLS / 2; ++k) asm volatile("" : "+f"(x[k].x), "+f"(x[k].y));   // not before the wait
+          if (!plain) {
 #pragma unroll
-          for (int k = 0; k < COLS; k += 2) {
-            if (k < clo || k >= chi) x[k / 2].x = -INFINITY;
-            if (k + 1 < clo || k + 1 >= chi) x[k / 2].y = -INFINITY;
+            for (int k = 0; k < COLS / 2; ++k) x[k] = make_float2(x[k].x * mu, x[k].y * mu);
           }
-        }
-        float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < COLS / 2; ++k) top = fmaxf(fmaxf(top, x[k].x), x[k].y);
-        // The running max moves only when a logit exceeds it by more than 2^14, or at
-        // the segment's first key; usually it stays, and then no max or sum is reduced.
-        if (softmax_sync_or(!ok_warp || fresh || top > kRescaleLog2)) {
+          for (int k = 0; k < COLS; k += 4) {
+            const float4 f = fac[k / 4], m = mr[k / 4];
+            x[k / 2] = fma2(x[k / 2], make_float2(f.x, f.y), make_float2(m.x, m.y));
+            x[k / 2 + 1] = fma2(x[k / 2 + 1], make_float2(f.z, f.w), make_float2(m.z, m.w));
+          }
+          if (!plain) {
+#pragma unroll
+            for (int k = 0; k < COLS; k += 2) {
+              if (k < clo || k >= chi) x[k / 2].x = -INFINITY;
+              if (k + 1 < clo || k + 1 >= chi) x[k / 2].y = -INFINITY;
+            }
+          }
+          if (moved) break;
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < COLS / 2; ++k) top = fmaxf(fmaxf(top, x[k].x), x[k].y);
+          // The running max moves only when a logit exceeds it by more than 2^14, or at
+          // the segment's first key; usually it stays, and then no max or sum is reduced.
+          if (!softmax_sync_or(!ok_warp || fresh || top > kRescaleLog2)) break;
           // a failed wait ends the role here, for all of its warps alike; O^T of the
           // tile before is complete from here on
           ok_warp = __all_sync(0xFFFFFFFFu, wait(&sm.p_free, (i & 1) ^ 1)) && ok_warp;
           if (softmax_sync_or(!ok_warp)) return false;
           tc_fence_after();
+          // the columns' maxima, from S once more: 16 columns at a time keep the code of
+          // what happens once or twice in a segment small
+#pragma unroll 1
+          for (int c0 = 0; c0 < COLS; c0 += 16) {
+            float2 y[8];
+            tmem_ld16_pairs(ts + c0, y);
+            tmem_ld_wait();
+            float t[16];
 #pragma unroll
-          for (int k = 0; k < COLS; k += 4) {
-            const float4 v = make_float4(warp_top(x[k / 2].x), warp_top(x[k / 2].y), warp_top(x[k / 2 + 1].x),
-                                         warp_top(x[k / 2 + 1].y));
-            if (lane == 0) *reinterpret_cast<float4*>(&sm.red[warp][k]) = v;
+            for (int k = 0; k < 16; k += 4) {
+              const float4 f = fac[(c0 + k) / 4], m = mr[(c0 + k) / 4];
+              asm volatile("" : "+f"(y[k / 2].x), "+f"(y[k / 2].y), "+f"(y[k / 2 + 1].x), "+f"(y[k / 2 + 1].y));
+              t[k] = fmaf(y[k / 2].x * mu, f.x, m.x);
+              t[k + 1] = fmaf(y[k / 2].y * mu, f.y, m.y);
+              t[k + 2] = fmaf(y[k / 2 + 1].x * mu, f.z, m.z);
+              t[k + 3] = fmaf(y[k / 2 + 1].y * mu, f.w, m.w);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (c0 + k < clo || c0 + k >= chi) t[k] = -INFINITY;
+            const float top16 = warp_reduce_many<16, true>(t, lane);
+            if ((lane & 1) == 0) sm.red[warp][c0 + (lane >> 1)] = top16;
           }
           softmax_sync();
           bool seen = false;
@@ -1190,54 +1138,51 @@ struct Softmax {
             const float t = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]), fmaxf(sm.red[2][tid], sm.red[3][tid]));
             seen = t != -INFINITY;
             // with one column every one that has grown moves, as the event is what costs
-            const float by = (fresh ? seen : t > 1.0f) ? t : 0.0f;
-            sm.neg_m[tid] -= by;
-            sm.red[0][tid] = -by;              // this thread alone has read the column's tops
-            sm.corr[tid] = fresh ? 1.0f : ex2(-by);
-            const uint32_t m = __ballot_sync(COLS < 32 ? 0xFFFFu : 0xFFFFFFFFu, by != 0.0f);
+            const float old = sm.neg_m[tid], now = old - ((fresh ? seen : t > 1.0f) ? t : 0.0f);
+            sm.neg_m[tid] = now;
+            sm.corr[tid] = fresh ? 1.0f : ex2(now - old);
+            const uint32_t m = __ballot_sync(COLS < 32 ? 0xFFFFu : 0xFFFFFFFFu, now != old);
             if (lane == 0) sm.moved[warp] = m;
           }
           const bool was_fresh = fresh;
           fresh = !softmax_sync_or(seen) && fresh;   // the new maxima are visible
-          const float4* mv = reinterpret_cast<const float4*>(sm.red[0]);
-          const float4* al = reinterpret_cast<const float4*>(sm.corr);
+          moved = true;
+          if (was_fresh) continue;
 #pragma unroll
           for (int k = 0; k < COLS; k += 4) {
-            const float4 d = mv[k / 4], f = al[k / 4];
-            x[k / 2] = add2(x[k / 2], make_float2(d.x, d.y));
-            x[k / 2 + 1] = add2(x[k / 2 + 1], make_float2(d.z, d.w));
+            const float4 f = al[k / 4];
             lpart[k / 2] = make_float2(lpart[k / 2].x * f.x, lpart[k / 2].y * f.y);
             lpart[k / 2 + 1] = make_float2(lpart[k / 2 + 1].x * f.z, lpart[k / 2 + 1].y * f.w);
           }
-          if (!was_fresh) {
 #pragma unroll 1
-            for (int j = 0; j < 2 * (COLS / 16); ++j) {   // 16 columns of two chunks
-              const int c0 = 16 * (j >> 1);
-              if (!((sm.moved[c0 / 32] >> (c0 & 31)) & 0xFFFFu)) continue;
-              const uint32_t ta = lane_off + 128 * (j & 1) + c0;
-              float2 v[2][8];
-              tmem_ld16_pairs(ta, v[0]);
-              tmem_ld16_pairs(ta + 64, v[1]);
-              tmem_ld_wait();
+          for (int j = 0; j < 2 * (COLS / 16); ++j) {   // 16 columns of two chunks
+            const int c0 = 16 * (j >> 1);
+            if (!((sm.moved[c0 / 32] >> (c0 & 31)) & 0xFFFFu)) continue;
+            const uint32_t ta = lane_off + 128 * (j & 1) + c0;
+            float2 v[2][8];
+            tmem_ld16_pairs(ta, v[0]);
+            tmem_ld16_pairs(ta + 64, v[1]);
+            tmem_ld_wait();
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t u[16];
+            for (int h = 0; h < 2; ++h) {
+              uint32_t u[16];
 #pragma unroll
-                for (int k = 0; k < 16; k += 4) {
-                  const float4 f = al[(c0 + k) / 4];
-                  asm volatile("" : "+f"(v[h][k / 2].x), "+f"(v[h][k / 2].y), "+f"(v[h][k / 2 + 1].x),
-                               "+f"(v[h][k / 2 + 1].y));   // not before the wait
-                  u[k] = __float_as_uint(v[h][k / 2].x * f.x);
-                  u[k + 1] = __float_as_uint(v[h][k / 2].y * f.y);
-                  u[k + 2] = __float_as_uint(v[h][k / 2 + 1].x * f.z);
-                  u[k + 3] = __float_as_uint(v[h][k / 2 + 1].y * f.w);
-                }
-                tmem_st16(ta + 64 * h, u);
+              for (int k = 0; k < 16; k += 4) {
+                const float4 f = al[(c0 + k) / 4];
+                asm volatile("" : "+f"(v[h][k / 2].x), "+f"(v[h][k / 2].y), "+f"(v[h][k / 2 + 1].x),
+                             "+f"(v[h][k / 2 + 1].y));   // not before the wait
+                u[k] = __float_as_uint(v[h][k / 2].x * f.x);
+                u[k + 1] = __float_as_uint(v[h][k / 2].y * f.y);
+                u[k + 2] = __float_as_uint(v[h][k / 2 + 1].x * f.z);
+                u[k + 3] = __float_as_uint(v[h][k / 2 + 1].y * f.w);
               }
+              tmem_st16(ta + 64 * h, u);
             }
-            tmem_st_wait();
           }
+          tmem_st_wait();
         }
+        tc_fence_before();
+        warp_arrive(&sm.s_free[i & 1], lane);
         uint32_t packed[COLS / 2];
 #pragma unroll
         for (int k = 0; k < COLS / 2; ++k) {
@@ -1262,12 +1207,12 @@ struct Softmax {
       }
       // ---- the columns' sums
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        float tmp[HB];
+      for (int n = 0; n < COLS; n += 16) {
+        float t[16];
 #pragma unroll
-        for (int k = 0; k < HB; ++k) tmp[k] = (k & 1) ? lpart[(n * HB + k) / 2].y : lpart[(n * HB + k) / 2].x;
-        const float sum = warp_reduce_many<HB, false>(tmp, lane);
-        if ((lane & ((1 << kShift) - 1)) == 0) sm.red[warp][n * HB + (lane >> kShift)] = sum;
+        for (int k = 0; k < 16; ++k) t[k] = (k & 1) ? lpart[(n + k) / 2].y : lpart[(n + k) / 2].x;
+        const float sum = warp_reduce_many<16, false>(t, lane);
+        if ((lane & 1) == 0) sm.red[warp][n + (lane >> 1)] = sum;
       }
       softmax_sync();
       if (tid < COLS) {
@@ -1288,9 +1233,7 @@ struct Softmax {
       prev_cols = cols;
       prev_slot = slot;
     }
-    const bool ok = flush();
-    if (warp == 0) bulk_wait_all();
-    return ok;
+    return true;
   }
 };
 
@@ -1327,7 +1270,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_attn(const __grid_constan
     }
     mbar_init(&sm.p_full, kSoftmaxWarps);
     mbar_init(&sm.p_free, 1);
+    mbar_init(&sm.q_raw, 32);
     mbar_init(&sm.q_full, kSoftmaxWarps);
+    mbar_init(&sm.q_free, 1);
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_free, kSoftmaxWarps);
     mbar_init(&sm.drain, 2);
@@ -1339,13 +1284,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_attn(const __grid_constan
     for (int i = tid; i < COLS * 16; i += kThreads) reinterpret_cast<uint4*>(sm.q_lo)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (warp == kMmaWarp) tmem_alloc(&sm.tmem_base, 512);
   const Share sh = find_share(a, G, *reinterpret_cast<ShareScratch*>(sm.p));
-  __syncthreads();                               // the zeros come before the low parts
-  {
-    // the first queries, by every warp; later ones by the softmax warps
-    Walk w;
-    if (w.first(a, G, sh) && w.settle(a, G)) load_queries<COLS, COLS / 16>(a, sm, w.gr, warp * (COLS / 16), COLS / 16);
-    fence_proxy_async_smem();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1375,6 +1313,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_attn(const __grid_constan
       if (!mbar_wait(&sm.drain, 0)) sm.abort = 1;
     } else if (warp == kMmaWarp + 2) {
       prefetch_tiles<COLS>(a, sm, sh, G);
+    } else {
+      fetch_queries<COLS>(a, sm, sh, G);
     }
   }
   __syncwarp();

@@ -100,8 +100,14 @@ __device__ __forceinline__ Group group_at(const DenseArgs& a, int r, int G) {
   q.tiles = (q.Wp + q.n + kTileKeys - 1) / kTileKeys;
   return q;
 }
-// A group of no tiles still takes one unit: its rows are written out empty.
-__device__ __forceinline__ int group_units(const Group& q) { return max(1, q.tiles); }
+// Units of work: a tile is one, and the step from one group to the next, which drains
+// the pipeline and fills it again, counts as kGap of them.  Without it a share of many
+// short groups takes far longer than one long group's: 2 x 999 rows of up to 8 tiles
+// took 391 us at 0, 218 at 2, 212 at 3, 214 at 4, 219 at 5; 128 rows of 24 to 260
+// tiles 473, 455, 452, 445, 433.  A group of no tiles takes one: its rows are
+// written out empty.
+constexpr int kGap = 4;
+__device__ __forceinline__ int group_units(const Group& q) { return q.tiles > 0 ? q.tiles + kGap : 1; }
 
 struct Share {
   int row, t0;                                   // the first group's row, and the share's first unit in it
@@ -178,9 +184,9 @@ __device__ __forceinline__ Share find_share(const DenseArgs& a, int G, ShareScra
     if (tid == kThreads - 1) s.total = upto;
     __syncthreads();
     const long long total = s.total;
-    per = (total + gridDim.x - 1) / gridDim.x;
+    per = (max(1ll, total - kGap) + gridDim.x - 1) / gridDim.x;   // nothing follows the last group
     lo = min(total, (long long)blockIdx.x * per);
-    units = min(total, lo + per) - lo;
+    units = (blockIdx.x + 1 == gridDim.x ? total : min(total, lo + per)) - lo;
     u = upto - sum;
     if (units == 0 || lo < u || lo >= upto) break;
   }
@@ -349,7 +355,7 @@ struct Walk {
       if (!next_segment(a, G)) return false;
     return true;
   }
-  __device__ __forceinline__ bool whole() const { return t0 == 0 && left >= group_units(gr); }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && left >= gr.tiles; }
 };
 
 // ---- dequantising ------------------------------------------------------------------------
@@ -839,47 +845,42 @@ __device__ __forceinline__ void convert_queries(const DenseArgs& a, Smem<COLS>& 
   constexpr int N = 2;                           // columns at a time
   const int c_lo = warp * (COLS / 4);
   const bool rope = a.rope_cos != nullptr && c_lo < gr.g * a.H;
-  float cs[16], sn[16];
-  if (rope && lane >= 28) {                      // the row's table entries of this lane's 16 dims
-    const size_t at = (size_t)(gr.p0 + c_lo / a.H) * 32 + 16 * (lane & 1);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      cs[i] = __ldg(a.rope_cos + at + i);
-      sn[i] = __ldg(a.rope_sin + at + i);
-    }
+  // the rotated pairs (448 + j, 480 + j) are one a lane, j = lane
+  float cs = 1.0f, sn = 0.0f;
+  if (rope) {
+    const size_t at = (size_t)(gr.p0 + c_lo / a.H) * 32 + lane;
+    cs = __ldg(a.rope_cos + at);
+    sn = __ldg(a.rope_sin + at);
   }
 #pragma unroll 1
   for (int c = c_lo; c < c_lo + COLS / 4; c += N) {
-    float f[N][16];
+    uint32_t w[N][8];
+    float big[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const uint8_t* src = sm.q + (lane >> 2) * (COLS * 128) + (c + j) * 128 + 32 * (lane & 3);
       const uint4 r0 = *reinterpret_cast<const uint4*>(src + 16 * ((lane >> 2) & 1));
       const uint4 r1 = *reinterpret_cast<const uint4*>(src + 16 * (((lane >> 2) & 1) ^ 1));
-      const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+      const uint32_t r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+      __nv_bfloat162 top = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&r[0]));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        f[j][2 * i] = __uint_as_float(w[i] << 16);
-        f[j][2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        w[j][i] = r[i];
+        if (i > 0) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&r[i])));
       }
+      big[j] = fmaxf(__low2float(top), __high2float(top));
     }
-    if (rope) {                                  // dims 448.. are lanes 28, 29 and 30, 31
+    float turned[N][2];
+    if (rope) {
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float other = __shfl_xor_sync(0xFFFFFFFFu, f[j][i], 2);
-          if (lane >= 28)
-            f[j][i] = lane < 30 ? __fsub_rn(__fmul_rn(f[j][i], cs[i]), __fmul_rn(other, sn[i]))
-                                : __fadd_rn(__fmul_rn(f[j][i], cs[i]), __fmul_rn(other, sn[i]));
-        }
-    }
-    float big[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      big[j] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) big[j] = fmaxf(big[j], fabsf(f[j][i]));
+      for (int j = 0; j < N; ++j) {
+        const uint8_t* src = sm.q + 7 * (COLS * 128) + (c + j) * 128 + 16 * ((lane >> 3) ^ 1) + 2 * (lane & 7);
+        const float x = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(src) << 16);
+        const float y = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(src + 64) << 16);
+        turned[j][0] = __fsub_rn(__fmul_rn(x, cs), __fmul_rn(y, sn));
+        turned[j][1] = __fadd_rn(__fmul_rn(y, cs), __fmul_rn(x, sn));
+        big[j] = fmaxf(lane < 28 ? big[j] : 0.0f, fmaxf(fabsf(turned[j][0]), fabsf(turned[j][1])));
+      }
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) big[j] = warp_top(big[j]);
@@ -892,20 +893,14 @@ __device__ __forceinline__ void convert_queries(const DenseArgs& a, Smem<COLS>& 
       const int e = (ex > 0 && ex < 255) ? max(ex - 127 - 7, -126) : 0;
       if (lane == 0) sm.factor[c + j] = a.softmax_scale * kLog2e * pow2(e);
       const float s1 = pow2(-e);
-      uint2 hi[4], lo[4];
+      uint2 hi[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {              // 4 dims at a time
-        const float x0 = f[j][4 * u] * s1, x1 = f[j][4 * u + 1] * s1;
-        const float x2 = f[j][4 * u + 2] * s1, x3 = f[j][4 * u + 3] * s1;
-        const __half2 h0 = __floats2half2_rn(x0, x1), h1 = __floats2half2_rn(x2, x3);
+        const uint32_t x = w[j][2 * u], y = w[j][2 * u + 1];
+        const __half2 h0 = __floats2half2_rn(__uint_as_float(x << 16) * s1, __uint_as_float(x & 0xFFFF0000u) * s1);
+        const __half2 h1 = __floats2half2_rn(__uint_as_float(y << 16) * s1, __uint_as_float(y & 0xFFFF0000u) * s1);
         hi[u].x = *reinterpret_cast<const uint32_t*>(&h0);
         hi[u].y = *reinterpret_cast<const uint32_t*>(&h1);
-        if (rope) {
-          const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-          const __half2 l0 = __floats2half2_rn(x0 - f0.x, x1 - f0.y), l1 = __floats2half2_rn(x2 - f1.x, x3 - f1.y);
-          lo[u].x = *reinterpret_cast<const uint32_t*>(&l0);
-          lo[u].y = *reinterpret_cast<const uint32_t*>(&l1);
-        }
       }
       // lanes of different atoms begin with different steps: their banks differ
       const int first = (lane & 1) | ((lane >> 2) & 2);
@@ -917,14 +912,22 @@ __device__ __forceinline__ void convert_queries(const DenseArgs& a, Smem<COLS>& 
         if (first & 2) swap2(hi[u], hi[u + 2]);
       const int place = (lane >> 1) & 3;         // as q_place has it for dims 16 (lane % 8) + 4 u; step 4 (lane % 2) + u
       uint8_t* dst = sm.q + (2 * (lane >> 3) + (lane & 1)) * (COLS * 128) + ((c + j) >> 3) * 1024 + 8 * (place & 1);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        *reinterpret_cast<uint2*>(dst + swz128((c + j) & 7, 2 * (u ^ first) + (place >> 1))) = hi[u];
-      if (rope && lane >= 28) {
-        uint8_t* low = sm.q_lo + (lane & 1) * (COLS * 128) + ((c + j) >> 3) * 1024 + 8 * (place & 1);
+      if (!rope || lane < 28) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<uint2*>(low + swz128((c + j) & 7, 2 * u + (place >> 1))) = lo[u];
+          *reinterpret_cast<uint2*>(dst + swz128((c + j) & 7, 2 * (u ^ first) + (place >> 1))) = hi[u];
+      }
+      if (rope) {
+        // q_place of dims 64 + lane and 96 + lane of chunk 3: places 2 and 3 of a step
+        const int at = (lane >> 4) * (COLS * 128) + ((c + j) >> 3) * 1024 +
+                       swz128((c + j) & 7, 2 * ((lane >> 2) & 3) + 1) + 2 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float x = turned[j][k] * s1;
+          const __half h = __float2half_rn(x), l = __float2half_rn(x - __half2float(h));
+          *reinterpret_cast<__half*>(sm.q + 6 * (COLS * 128) + at + 8 * k) = h;
+          *reinterpret_cast<__half*>(sm.q_lo + at + 8 * k) = l;
+        }
       }
     }
   }
@@ -1007,8 +1010,11 @@ struct Softmax {
       const bool whole = w.whole();
       const int slot = whole ? -1 : (w.t0 > 0 ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1);
       if (more && !whole && w.t0 == 0)
-        rec = make_int4(w.gr.r0, w.gr.g, blockIdx.x, blockIdx.x + (group_units(w.gr) - w.left + sh.per - 1) / sh.per);
-      if (more && w.t >= w.t_end) {              // rows that see nothing
+        rec = make_int4(w.gr.r0, w.gr.g, blockIdx.x,
+                        min((int)gridDim.x - 1, (int)blockIdx.x + (w.gr.tiles - w.left + sh.per - 1) / sh.per));
+      if (more && w.t >= w.t_end) {
+        if (w.gr.tiles > 0) continue;            // the share begins behind the group's last tile
+        // rows that see nothing
         if (!row_valid(a, w.gr.b, w.gr.p0) && tid == 0) raise_flag(a.status, CSA_FLAG_ROW_INVALID);
         uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)w.gr.r0 * a.H * D);
         for (int k = tid; k < cols * (D / 8); k += 32 * kSoftmaxWarps) dst[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -1327,39 +1333,145 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_attn(const __grid_constan
   }
 }
 
-// Joins the parts of the groups cut between CTAs: one CTA per (cut, column),
-// thread = 4 dims; O = sum_q 2^(m_q - M) O_q / sum_q 2^(m_q - M) l_q in CTA order.
-__global__ void __launch_bounds__(128) k_dense_merge(DenseArgs a, int cols_max) {
-  pdl_wait();
-  const int4 rec = __ldcg(a.rec + blockIdx.x);
-  const int c = blockIdx.y;
-  if (rec.x < 0 || c >= rec.y * a.H) return;
-  const int n = rec.w - rec.z + 1;               // parts: slot 2 c0 + 1, then 2 (c0 + 1), 2 (c0 + 2), ...
-  auto slot = [&](int q) { return q == 0 ? 2 * rec.z + 1 : 2 * (rec.z + q); };
-  float M = kNoMax;
-  for (int q = 0; q < n; ++q) M = fmaxf(M, __ldcg(a.part_ml + (size_t)slot(q) * 2 * cols_max + c));
-  float L = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-  for (int q = 0; q < n; ++q) {
-    const float* ml = a.part_ml + (size_t)slot(q) * 2 * cols_max + c;
-    const float m = __ldcg(ml), l = __ldcg(ml + cols_max);
-    const float w = ex2(m - M);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + ((size_t)slot(q) * cols_max + c) * D) + threadIdx.x);
-    L += w * l;
-    o.x += w * v.x;
-    o.y += w * v.y;
-    o.z += w * v.z;
-    o.w += w * v.w;
-  }
+// Joins the parts of the groups cut between CTAs:
+// O = sum_q 2^(m_q - M) O_q / sum_q 2^(m_q - M) l_q.  One wave of CTAs, each of one
+// column (a CTA for every cut and column spent most of its time on being launched and
+// finding nothing to do).  Thread = 4 dims.  A cut of few parts is the work of a
+// quarter of a CTA, which needs no barrier; of one of many parts each quarter sums
+// every fourth, and the four sums are joined in a fixed order.
+constexpr int kMergeSplit = 4, kMergeLoads = 8, kMergeThreads = 128 * kMergeSplit;
+__device__ __forceinline__ void merge_store(const DenseArgs& a, size_t col, int d, float M, float L, float4 o) {
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
   uint2 st;
   st.x = *reinterpret_cast<const uint32_t*>(&x);
   st.y = *reinterpret_cast<const uint32_t*>(&y);
-  const size_t col = (size_t)rec.x * a.H + c;
-  *(reinterpret_cast<uint2*>(a.out + col * D) + threadIdx.x) = st;
-  if (a.lse && threadIdx.x == 0) a.lse[col] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+  *(reinterpret_cast<uint2*>(a.out + col * D) + d) = st;
+  if (a.lse && d == 0) a.lse[col] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+__device__ __forceinline__ void add_scaled(float4& o, float w, const float4& v) {
+  o.x += w * v.x;
+  o.y += w * v.y;
+  o.z += w * v.z;
+  o.w += w * v.w;
+}
+__global__ void __launch_bounds__(kMergeThreads, 2) k_dense_merge(DenseArgs a, int cols_max, int num_recs) {
+  __shared__ int4 s_rec[kMergeThreads];          // cuts of few parts from the front, of many from the back
+  __shared__ int2 s_count[kMergeThreads / 32];   // of each kind, by warp
+  __shared__ float s_w[kMergeThreads];           // a group has at most one part per SM
+  __shared__ float s_m[kMergeThreads / 32], s_l[kMergeThreads / 32];
+  __shared__ float4 s_o[kMergeSplit - 1][128];
+  const int tid = threadIdx.x, k = tid >> 7, d = tid & 127, c = blockIdx.y;
+  pdl_wait();
+  // the cuts of this column, in the same order in every CTA that shares them out
+  const int4 mine = tid < num_recs ? __ldcg(a.rec + tid) : make_int4(-1, 0, 0, 0);
+  const bool used = mine.x >= 0 && c < mine.y * a.H, is_few = mine.w - mine.z < kMergeLoads;
+  const uint32_t b_few = __ballot_sync(0xFFFFFFFFu, used && is_few), b_many = __ballot_sync(0xFFFFFFFFu, used && !is_few);
+  if (lane_id() == 0) s_count[tid >> 5] = make_int2(__popc(b_few), __popc(b_many));
+  __syncthreads();
+  int few = 0, many = 0, at_few = 0, at_many = 0;
+#pragma unroll
+  for (int w = 0; w < kMergeThreads / 32; ++w) {
+    if (w == tid >> 5) {
+      at_few = few;
+      at_many = many;
+    }
+    few += s_count[w].x;
+    many += s_count[w].y;
+  }
+  const uint32_t below = (1u << lane_id()) - 1u;
+  if (used) s_rec[is_few ? at_few + __popc(b_few & below) : kMergeThreads - 1 - at_many - __popc(b_many & below)] = mine;
+  __syncthreads();
+  // a part's slot: 2 c0 + 1 of the first, then 2 (c0 + 1), 2 (c0 + 2), ...
+  auto slot = [](const int4& rec, int q) { return (size_t)(q == 0 ? 2 * rec.z + 1 : 2 * (rec.z + q)); };
+  const float* part = a.part + (size_t)c * D + 4 * d;
+#pragma unroll 1
+  for (int i = blockIdx.x * kMergeSplit + k; i < few; i += gridDim.x * kMergeSplit) {
+    const int4 rec = s_rec[i];
+    const int n = rec.w - rec.z + 1;
+    float4 v[kMergeLoads];
+    float m[kMergeLoads], l[kMergeLoads], M = kNoMax;
+#pragma unroll
+    for (int q = 0; q < kMergeLoads; ++q) {
+      v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      m[q] = kNoMax;
+      l[q] = 0.0f;
+      if (q < n) {
+        const float* ml = a.part_ml + slot(rec, q) * 2 * cols_max + c;
+        m[q] = __ldcg(ml);
+        l[q] = __ldcg(ml + cols_max);
+        v[q] = __ldcg(reinterpret_cast<const float4*>(part + slot(rec, q) * cols_max * D));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kMergeLoads; ++q) M = fmaxf(M, m[q]);
+    float L = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int q = 0; q < kMergeLoads; ++q) {
+      if (q < n) {
+        const float w = ex2(m[q] - M);
+        L += w * l[q];
+        add_scaled(o, w, v[q]);
+      }
+    }
+    merge_store(a, (size_t)rec.x * a.H + c, d, M, L, o);
+  }
+#pragma unroll 1
+  for (int i = blockIdx.x; i < many; i += gridDim.x) {
+    const int4 rec = s_rec[kMergeThreads - 1 - i];
+    const int n = rec.w - rec.z + 1;
+    float m = kNoMax, l = 0.0f;
+    if (tid < n) {
+      const float* ml = a.part_ml + slot(rec, tid) * 2 * cols_max + c;
+      m = __ldcg(ml);
+      l = __ldcg(ml + cols_max);
+    }
+    float4 v[kMergeLoads];
+    auto load = [&](int q0) {
+#pragma unroll
+      for (int j = 0; j < kMergeLoads; ++j) {
+        const int q = q0 + j * kMergeSplit;
+        v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (q < n) v[j] = __ldcg(reinterpret_cast<const float4*>(part + slot(rec, q) * cols_max * D));
+      }
+    };
+    load(k);                                     // before the weights are known
+    const float m_warp = warp_top(m);
+    if (lane_id() == 0) s_m[tid >> 5] = m_warp;
+    __syncthreads();
+    float M = s_m[0];
+#pragma unroll
+    for (int w = 1; w < kMergeThreads / 32; ++w) M = fmaxf(M, s_m[w]);
+    const float weight = ex2(m - M);
+    s_w[tid] = tid < n ? weight : 0.0f;
+    float l_warp = weight * l;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l_warp += __shfl_xor_sync(0xFFFFFFFFu, l_warp, x);
+    if (lane_id() == 0) s_l[tid >> 5] = l_warp;
+    __syncthreads();
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int q0 = k; q0 < n; q0 += kMergeLoads * kMergeSplit) {
+      if (q0 != k) load(q0);
+#pragma unroll
+      for (int j = 0; j < kMergeLoads; ++j) {
+        const int q = q0 + j * kMergeSplit;
+        if (q < n) add_scaled(o, s_w[q], v[j]);
+      }
+    }
+    if (k > 0) s_o[k - 1][d] = o;
+    __syncthreads();
+    if (k == 0) {
+      float L = s_l[0];
+#pragma unroll
+      for (int w = 1; w < kMergeThreads / 32; ++w) L += s_l[w];
+#pragma unroll
+      for (int j = 1; j < kMergeSplit; ++j) add_scaled(o, 1.0f, s_o[j - 1][d]);
+      merge_store(a, (size_t)rec.x * a.H + c, d, M, L, o);
+    }
+    __syncthreads();                             // the next cut uses the same places
+  }
 }
 
 constexpr size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -1373,19 +1485,21 @@ int group_cols(int rows, int H) {
 
 // CTAs: one per SM, no more than the tiles that the host's bounds allow.
 int dense_grid(int num_rows, int max_entries, int num_sms) {
-  const int64_t tiles = ((int64_t)max_entries + 2 * WIN + kTileKeys - 1) / kTileKeys;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(num_sms, tiles * num_rows));
+  const int64_t tiles = ((int64_t)max_entries + kTileKeys - 1) / kTileKeys + 2;   // a group's window: at most two
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(num_sms, kMergeThreads), tiles * num_rows));
 }
 
 template <int COLS>
-cudaError_t launch_cols(DenseArgs a, int grid, cudaStream_t stream) {
+cudaError_t launch_cols(DenseArgs a, int grid, int num_sms, cudaStream_t stream) {
   static_assert(sizeof(Smem<COLS>) <= 232448, "shared memory of one CTA");
   const size_t smem = sizeof(Smem<COLS>);
   cudaError_t e = cudaFuncSetAttribute(k_dense_attn<COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   e = launch_kernel(Order::kStream, k_dense_attn<COLS>, dim3(grid), dim3(kThreads), smem, stream, a);
   if (e != cudaSuccess || grid == 1) return e;
-  return launch_kernel(Order::kChained, k_dense_merge, dim3(grid - 1, COLS), dim3(128), 0, stream, a, COLS);
+  // two CTAs fit an SM, and a grid has a CTA per SM at most
+  const dim3 merge(std::max(1, 2 * num_sms / COLS), COLS);
+  return launch_kernel(Order::kChained, k_dense_merge, merge, dim3(kMergeThreads), 0, stream, a, COLS, grid - 1);
 }
 
 }  // namespace
@@ -1405,9 +1519,9 @@ cudaError_t launch_dense_attn(DenseArgs a, void* ws, int num_sms, cudaStream_t s
   p += up256((size_t)2 * grid * 2 * cols * sizeof(float));
   a.part = reinterpret_cast<float*>(p);
   switch (cols) {
-    case 16: return launch_cols<16>(a, grid, stream);
-    case 32: return launch_cols<32>(a, grid, stream);
-    default: return launch_cols<64>(a, grid, stream);
+    case 16: return launch_cols<16>(a, grid, num_sms, stream);
+    case 32: return launch_cols<32>(a, grid, num_sms, stream);
+    default: return launch_cols<64>(a, grid, num_sms, stream);
   }
 }
 

@@ -486,46 +486,50 @@ struct Dequant {
     const int c = 2 * wg + h;
     const bool turn = c == 3 && q >= 2 && a.rope_cos != nullptr;
     if (!values && c == 0 && lane == 0) sm.odd[tile & 1][key0 >> 5] = 1u;
+    // the four rows' codes, before the wait
+    uint4 u[4], v[4];
+    float ws[4];
+    const uint8_t* src[4];
+    int at = (wlo + ki) % a.win_cap;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      u[s] = v[s] = make_uint4(0u, 0u, 0u, 0u);
+      ws[s] = 0.0f;
+      const size_t ring = (size_t)b * a.win_cap + at;
+      src[s] = a.win_codes + ring * D + c * 128 + 32 * q;
+      if (ki + 8 * s < W) {
+        u[s] = ldg_nc_v4(src[s]);
+        v[s] = ldg_nc_v4(src[s] + 16);
+        ws[s] = ldg_nc_f32(a.win_scale + ring);
+      }
+      at += 8;
+      while (at >= a.win_cap) at -= a.win_cap;
+    }
     const bool ok = wait_or_abort(values ? &sm.v_free[c] : &sm.k_free[wg], values ? (tile & 1) ^ 1 : h ^ 1,
                                   a.wait_budget, &sm.abort);
     if (!__all_sync(0xFFFFFFFFu, ok)) return false;
     tc_fence_after();
-#pragma unroll 1
-    for (int s0 = 0; s0 < 4; s0 += 2) {          // two rows, r and r + 8
-      uint4 u[2], v[2], pu[2], pv[2];            // 32 codes, and the rotation's other half
-      float ws[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        u[j] = v[j] = pu[j] = pv[j] = make_uint4(0u, 0u, 0u, 0u);
-        ws[j] = 0.0f;
-        const int k = ki + 8 * (s0 + j);
-        if (k < W) {
-          const size_t ring = (size_t)b * a.win_cap + (size_t)((wlo + k) % a.win_cap);
-          const uint8_t* src = a.win_codes + ring * D + c * 128 + 32 * q;
-          u[j] = ldg_nc_v4(src);
-          v[j] = ldg_nc_v4(src + 16);
-          if (turn) {                            // dims 448 + 32 (q - 2): the halves are q = 2 and 3
-            pu[j] = ldg_nc_v4(src + 32 * (5 - 2 * q));
-            pv[j] = ldg_nc_v4(src + 32 * (5 - 2 * q) + 16);
-          }
-          ws[j] = __ldg(a.win_scale + ring);
-        }
-      }
+    for (int s0 = 0; s0 < 4; s0 += 2) {          // two rows, r and r + 8
       uint32_t o[2][16];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int k = ki + 8 * (s0 + j);
-        const int ex = ws[j] > 0.0f ? min(7, max(-14, (int)(__float_as_uint(ws[j]) >> 23) - 127)) : -14;
+        const float scale = ws[s0 + j];
+        const int ex = scale > 0.0f ? min(7, max(-14, (int)(__float_as_uint(scale) >> 23) - 127)) : -14;
         const float pw = pow2(ex);
         if (turn && k < W) {
-          const size_t at = (size_t)(wlo + k) * 32;
+          const size_t row = (size_t)(wlo + k) * 32;
           uint32_t t[16];
-          rotate_window(a.rope_cos + at, a.rope_sin + at, q == 2, pw, u[j], v[j], pu[j], pv[j], t);
+          const uint8_t* other = src[s0 + j] + 32 * (5 - 2 * q);   // dims 448 + 32 (q - 2): the halves are q = 2 and 3
+          rotate_window(a.rope_cos + row, a.rope_sin + row, q == 2, pw, u[s0 + j], v[s0 + j], ldg_nc_v4(other),
+                        ldg_nc_v4(other + 16), t);
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[j][i] = t[i];
         } else {
           const __half2 hp = __float2half2_rn(pw);
-          const uint32_t cw[8] = {u[j].x, u[j].y, u[j].z, u[j].w, v[j].x, v[j].y, v[j].z, v[j].w};
+          const uint4 x = u[s0 + j], y = v[s0 + j];
+          const uint32_t cw[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             uint32_t f[2];
@@ -534,7 +538,7 @@ struct Dequant {
             o[j][2 * i + 1] = hmul2_u32(f[1], hp);
           }
         }
-        if (!values && c == 0 && q == 0) sm.mu[tile & 1][key0 + 8 * (s0 + j)] = k < W ? ws[j] * pow2(-ex) : -1.0f;
+        if (!values && c == 0 && q == 0) sm.mu[tile & 1][key0 + 8 * (s0 + j)] = k < W ? scale * pow2(-ex) : -1.0f;
       }
       __syncwarp();
       if (!values) {

@@ -273,3 +273,53 @@ def test_same_bits_again_without_lse_on_another_stream_and_from_a_graph():
         outs.append(c.out.clone())
     assert csa.csa_check_device_status(c.ws) == (0, 0)
     assert torch.equal(outs[1], first) and torch.equal(outs[0], outs[2]) and not torch.equal(outs[0], first)
+
+
+@gpu
+@pytest.mark.parametrize("H", [16, 32, 64])
+def test_cuts_of_few_and_of_many_parts_join_the_same_way_every_time(H):
+    """A few long rows among many short ones: some groups are cut into dozens of
+    parts, some into two, and the joined bits do not depend on the run."""
+    ctx = [70001, 30000, 9000] + [700] * 60 + [24000]
+    c = Case(160 + H, ctx, 1, 128)
+    req, pos = list(range(64)), [x - 1 for x in ctx]
+    q = c.queries(64, H)
+    assert c.run(csa, req, pos, H, q) == (0, 0)
+    c.check(req, pos, H, q, rows=[0, 1, 2, 3, 33, 62, 63])
+    first, lse = c.out.clone(), c.lse.clone()
+    for _ in range(20):
+        c.out.fill_(7.0)
+        c.ws[256:] = 255
+        c.call()
+        assert torch.equal(c.out, first) and torch.equal(c.lse, lse)
+
+
+@gpu
+def test_rows_behind_the_last_stay_as_they_were():
+    c = Case(170, [513, 40, 129], 2, 130)
+    q = c.queries(3, 32)
+    assert c.run(csa, [0, 1, 2], [512, 39, 128], 32, q) == (0, 0)
+    assert (c.out[3:] == 7.0).all() and (c.lse[3:] == 7.0).all()
+
+
+@gpu
+@pytest.mark.parametrize("H", [16, 64])
+def test_wait_budget_runs_out_and_the_next_call_is_exact(H):
+    """Every wait of the pipeline is bounded: a call whose waits run out returns,
+    says so, and leaves nothing behind for the next one."""
+    c = Case(180 + H, [5000, 300, 2, 900], 2, 128)
+    req, pos = [0, 1, 2, 3], [4999, 299, 1, 899]
+    q = c.queries(4, H)
+    assert c.run(csa, req, pos, H, q) == (0, 0)
+    first = c.out.clone()
+    csa.csa_set_wait_budget(200)                          # SM clocks: shorter than any fetch
+    try:
+        c.call()
+        rc, flags = csa.csa_check_device_status(c.ws)
+        assert rc == 6 and flags & csa.FLAG_TIMEOUT
+    finally:
+        csa.csa_set_wait_budget(0)
+    c.ws[:256] = 0
+    c.out.fill_(7.0)
+    c.call()
+    assert csa.csa_check_device_status(c.ws) == (0, 0) and torch.equal(c.out, first)

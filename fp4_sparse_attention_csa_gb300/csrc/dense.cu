@@ -26,12 +26,10 @@
 // and k_dense_merge joins them in CTA order.
 //
 // Pipeline.  One CTA per SM, three roles that meet only at mbarriers:
-//   8 dequantising warps (two warpgroups, 128 dims of a tile at a time each),
-//   4 softmax warps (32 keys x all columns each), also queries and output,
-//   2 warps that issue the MMAs, one for each product, and one that prefetches
-//   entries into L2.
-// The tensor pipe takes 48 clocks per M128 K16 MMA up to N = 64 (64 at N = 128),
-// so a tile costs at least 64 x 48 = 3072; the roles have to hide behind that.
+//   8 dequantising warps (two warpgroups, two 128-dim chunks of a tile each),
+//   8 softmax warps (32 keys x half of the columns each), also queries and output,
+//   2 warps that issue the MMAs, one for each product, one that prefetches entries
+//   into L2, and one that fetches the next queries.
 // Shared memory holds Q (64 KB), P and one fp16 tile (128 KB), not two.  So the
 // first product does not read it: the dequantising warps write each 128-dim chunk
 // to tensor memory (two 64-column slots) as its A operand, and S of tile t + 1 is
@@ -39,6 +37,22 @@
 // warpgroup's two chunks the first waits in registers and the second in its slot
 // until the second product has used tile t's.  That also takes 4 of the 6 KB per
 // MMA off the shared-memory port, which the second product alone fills.
+//
+// What bounds it.  At N = 64 an MMA of M128 K16 takes 32 clocks with A in tensor
+// memory and 48 with both operands in shared memory: a tile's 64 take 2700 clocks
+// together.  A tile takes 5600: its shared-memory traffic (second product 1540, first
+// product's Q 510, values stored 1150, the rest 300) fills the port for 3500, and the
+// loads and stores queue behind the second product's, which lengthens the chain of
+// two tiles (convert, S, softmax, O^T, store) that one tile of space allows.  64 x 4096
+// queries over 4 long caches run at 750 TFLOP/s, 128 rows over 128 caches at 740, 0.40 of
+// what cuBLAS reaches in bf16.  A step between groups costs about four tiles more
+// (queries in, first maximum, output); one token of 4096 is all such steps.
+// One kernel is 128 KB of code and the parts that run once per group are fetched
+// cold, at several clocks per instruction; loops there stay rolled.
+// Measured on the way (128 rows over 128 caches, us): one serial role per tile 868;
+// three roles, S from tensor memory 569; MMA loops rolled 488; entry tiles aligned to
+// pages, output by plain stores 485; the list of work with the steps' cost, cuts joined
+// in one wave 428; 8 softmax warps for 4: 419 (2 x 999 rows: 535, 580, 595, 435, 202, 187).
 #include <algorithm>
 
 #include "attn_device.cuh"
@@ -48,7 +62,7 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 512;                    // 8 dequantising, 4 softmax, 2 MMA, 1 prefetching warp (and 1 idle)
+constexpr int kThreads = 640;                    // 8 dequantising, 8 softmax, 2 MMA, 1 prefetching, 1 query-fetching warp
 constexpr int kTileKeys = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -198,7 +212,11 @@ __device__ __forceinline__ Share find_share(const DenseArgs& a, int G, ShareScra
 }
 
 // ---- shared memory ---------------------------------------------------------------------
-constexpr int kDequantWarps = 8, kSoftmaxWarps = 4;
+constexpr int kDequantWarps = 8, kSoftmaxWarps = 8;
+// Of the softmax warps those that work: two for each quarter of the keys, half of the
+// columns each, but no fewer than 16.
+template <int COLS>
+constexpr int kSoftmaxUsed = COLS < 32 ? 4 : kSoftmaxWarps;
 constexpr int kMmaWarp = kDequantWarps + kSoftmaxWarps;
 constexpr float kNoMax = -3e38f;                 // running max of a column that has seen nothing
 
@@ -311,14 +329,18 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, lo
   return true;
 }
 // The softmax warps' barriers.
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int COLS>
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftmaxUsed<COLS>) : "memory");
+}
+template <int COLS>
 __device__ __forceinline__ bool softmax_sync_or(bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, 2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "bar.red.or.pred p, 2, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)v)
+      : "r"((uint32_t)v), "n"(32 * kSoftmaxUsed<COLS>)
       : "memory");
   return r != 0;
 }
@@ -842,12 +864,13 @@ __device__ __forceinline__ void fetch_queries(const DenseArgs& a, Smem<COLS>& sm
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// A softmax warp's quarter of the columns to fp16, in place: a column's 512 dims are
+// A softmax warp's share of the columns to fp16, in place: a column's 512 dims are
 // one warp's, 16 consecutive ones a lane, and are all read before any is written.
 template <int COLS>
 __device__ __forceinline__ void convert_queries(const DenseArgs& a, Smem<COLS>& sm, const Group& gr, int warp, int lane) {
   constexpr int N = 2;                           // columns at a time
-  const int c_lo = warp * (COLS / 4);
+  constexpr int kMine = COLS / kSoftmaxUsed<COLS>;
+  const int c_lo = warp * kMine;
   const bool rope = a.rope_cos != nullptr && c_lo < gr.g * a.H;
   // the rotated pairs (448 + j, 480 + j) are one a lane, j = lane
   float cs = 1.0f, sn = 0.0f;
@@ -857,7 +880,7 @@ __device__ __forceinline__ void convert_queries(const DenseArgs& a, Smem<COLS>& 
     sn = __ldg(a.rope_sin + at);
   }
 #pragma unroll 1
-  for (int c = c_lo; c < c_lo + COLS / 4; c += N) {
+  for (int c = c_lo; c < c_lo + kMine; c += N) {
     uint32_t w[N][8];
     float big[N];
 #pragma unroll
@@ -946,11 +969,14 @@ __device__ __forceinline__ void convert_queries(const DenseArgs& a, Smem<COLS>& 
 template <int COLS, bool kParts>
 __device__ __forceinline__ void write_out(const DenseArgs& a, Smem<COLS>& sm, int warp, int lane, int r0, int cols,
                                           int slot) {
-  const int d = 32 * warp + (lane ^ (8 * (warp & 2)));   // the lane's dim in a chunk, as the tile was laid out
+  const int quarter = warp & 3;
+  const int d = 32 * quarter + (lane ^ (8 * (quarter & 2)));   // the lane's dim in a chunk, as the tile was laid out
+  // with two warps for a quarter of the dims, each takes two of the four chunks
+  constexpr int kStep = kSoftmaxUsed<COLS> / 4;
 #pragma unroll 1
-  for (int j = 0; j < cols / 8; ++j) {           // 16 columns of two chunks
+  for (int j = kStep > 1 ? warp >> 2 : 0; j < cols / 8; j += kStep) {   // 16 columns of two chunks
     const int c0 = 16 * (j >> 1), dc = 2 * (j & 1);
-    const uint32_t ta = 64 * dc + ((uint32_t)(32 * warp) << 16) + c0;
+    const uint32_t ta = 64 * dc + ((uint32_t)(32 * quarter) << 16) + c0;
     uint32_t v[2][16];
     tmem_ld16(ta, v[0]);
     tmem_ld16(ta + 64, v[1]);
@@ -986,7 +1012,8 @@ struct Softmax {
   using S = Smem<COLS>;
   const DenseArgs& a;
   S& sm;
-  int lane, warp;                                // warp 0..3: 32 keys, and 32 dims of each chunk
+  int lane, warp;                                // 32 keys (warp % 4) and, of the tile, kCols columns (warp / 4)
+  static constexpr int kCols = 4 * COLS / kSoftmaxUsed<COLS>;
 
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     return wait_or_abort(bar, parity, a.wait_budget, &sm.abort);
@@ -1005,8 +1032,9 @@ struct Softmax {
     Walk w;
     uint32_t i = 0, outs = 0, segs = 0;
     int prev_r0 = -1, prev_cols = 0, prev_slot = 0;
-    const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
-    const int mykey = 32 * warp + lane, tid = mykey;
+    const int quarter = warp & 3, cb = warp >> 2 ? kCols : 0;   // the first column
+    const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+    const int mykey = 32 * quarter + lane, tid = 32 * warp + lane;
     bool more = w.first(a, G, sh);
 #pragma unroll 1
     for (;; more = w.next_segment(a, G)) {
@@ -1021,7 +1049,7 @@ struct Softmax {
         // rows that see nothing
         if (!row_valid(a, w.gr.b, w.gr.p0) && tid == 0) raise_flag(a.status, CSA_FLAG_ROW_INVALID);
         uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)w.gr.r0 * a.H * D);
-        for (int k = tid; k < cols * (D / 8); k += 32 * kSoftmaxWarps) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+        for (int k = tid; k < cols * (D / 8); k += 32 * kSoftmaxUsed<COLS>) dst[k] = make_uint4(0u, 0u, 0u, 0u);
         if (a.lse && tid < cols) a.lse[(size_t)w.gr.r0 * a.H + tid] = -INFINITY;
         continue;
       }
@@ -1031,11 +1059,11 @@ struct Softmax {
         if (tid < COLS) sm.neg_m[tid] = 0.0f;
         fence_proxy_async_smem();
         warp_arrive(&sm.q_full, lane);
-        softmax_sync();                          // factors and maxima visible to all softmax warps
+        softmax_sync<COLS>();                    // factors and maxima visible to all softmax warps
       }
       if (prev_r0 >= 0) {                        // the segment before, once its last O^T is complete
         const bool ok = wait(&sm.o_full, outs & 1);
-        if (softmax_sync_or(!ok)) return false;
+        if (softmax_sync_or<COLS>(!ok)) return false;
         ++outs;
         tc_fence_after();
         if (prev_slot < 0) write_out<COLS, false>(a, sm, warp, lane, prev_r0, prev_cols, 0);
@@ -1048,22 +1076,22 @@ struct Softmax {
       bool fresh = true;                         // no key of the segment seen yet: neg_m is not a max
       // keys that every column sees (window keys aside); none when columns are unused
       const int all_see = cols == COLS ? w.gr.Wp + entries_at(a, w.gr.p0) : 0;
-      float2 lpart[COLS / 2];                    // this key's share of the columns' sums of p
+      float2 lpart[kCols / 2];                   // this key's share of the columns' sums of p
 #pragma unroll
-      for (int k = 0; k < COLS / 2; ++k) lpart[k] = make_float2(0.0f, 0.0f);
+      for (int k = 0; k < kCols / 2; ++k) lpart[k] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
       for (; w.t < w.t_end; ++w.t, ++i) {
         const bool ok = wait(&sm.s_full[i & 1], (i >> 1) & 1);
         bool ok_warp = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
-        const uint32_t ts = kTmemS + 64 * (i & 1) + lane_off;
+        const uint32_t ts = kTmemS + 64 * (i & 1) + cb + lane_off;
         // the columns that see this key; usually all, and none is a window key
         const int ki = w.t * kTileKeys + mykey;
-        int clo = 0, chi = COLS;
+        int clo = 0, chi = kCols;                 // from cb on
         float mu = 1.0f;
-        const bool plain = (w.t + 1) * kTileKeys <= all_see && !sm.odd[i & 1][warp];
+        const bool plain = (w.t + 1) * kTileKeys <= all_see && !sm.odd[i & 1][quarter];
         if (!plain) {
-          if (sm.odd[i & 1][warp]) mu = sm.mu[i & 1][mykey];
+          if (sm.odd[i & 1][quarter]) mu = sm.mu[i & 1][mykey];
           int ilo = 0, ihi = -1;                 // rows of the group
           if (mu >= 0.0f) {
             if (ki < w.gr.Wp) {
@@ -1074,35 +1102,35 @@ struct Softmax {
               ihi = w.gr.g - 1;
             }
           }
-          clo = ilo * a.H;
-          chi = (ihi + 1) * a.H;
+          clo = ilo * a.H - cb;
+          chi = (ihi + 1) * a.H - cb;
         }
-        const float4* fac = reinterpret_cast<const float4*>(sm.factor);
-        const float4* mr = reinterpret_cast<const float4*>(sm.neg_m);
-        const float4* al = reinterpret_cast<const float4*>(sm.corr);
-        float2 x[COLS / 2];
+        const float4* fac = reinterpret_cast<const float4*>(sm.factor + cb);
+        const float4* mr = reinterpret_cast<const float4*>(sm.neg_m + cb);
+        const float4* al = reinterpret_cast<const float4*>(sm.corr + cb);
+        float2 x[kCols / 2];
         bool moved = false;
 #pragma unroll 1
         for (;;) {                               // again once the running max has moved
           // x = logit - m; a column that does not see the key: -inf
 #pragma unroll
-          for (int k = 0; k < COLS; k += 16) tmem_ld16_pairs(ts + k, &x[k / 2]);
+          for (int k = 0; k < kCols; k += 16) tmem_ld16_pairs(ts + k, &x[k / 2]);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < COLS / 2; ++k) asm volatile("" : "+f"(x[k].x), "+f"(x[k].y));   // not before the wait
+          for (int k = 0; k < kCols / 2; ++k) asm volatile("" : "+f"(x[k].x), "+f"(x[k].y));   // not before the wait
           if (!plain) {
 #pragma unroll
-            for (int k = 0; k < COLS / 2; ++k) x[k] = make_float2(x[k].x * mu, x[k].y * mu);
+            for (int k = 0; k < kCols / 2; ++k) x[k] = make_float2(x[k].x * mu, x[k].y * mu);
           }
 #pragma unroll
-          for (int k = 0; k < COLS; k += 4) {
+          for (int k = 0; k < kCols; k += 4) {
             const float4 f = fac[k / 4], m = mr[k / 4];
             x[k / 2] = fma2(x[k / 2], make_float2(f.x, f.y), make_float2(m.x, m.y));
             x[k / 2 + 1] = fma2(x[k / 2 + 1], make_float2(f.z, f.w), make_float2(m.z, m.w));
           }
           if (!plain) {
 #pragma unroll
-            for (int k = 0; k < COLS; k += 2) {
+            for (int k = 0; k < kCols; k += 2) {
               if (k < clo || k >= chi) x[k / 2].x = -INFINITY;
               if (k + 1 < clo || k + 1 >= chi) x[k / 2].y = -INFINITY;
             }
@@ -1110,19 +1138,19 @@ struct Softmax {
           if (moved) break;
           float top = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < COLS / 2; ++k) top = fmaxf(fmaxf(top, x[k].x), x[k].y);
+          for (int k = 0; k < kCols / 2; ++k) top = fmaxf(fmaxf(top, x[k].x), x[k].y);
           // The running max moves only when a logit exceeds it by more than 2^14, or at
           // the segment's first key; usually it stays, and then no max or sum is reduced.
-          if (!softmax_sync_or(!ok_warp || fresh || top > kRescaleLog2)) break;
+          if (!softmax_sync_or<COLS>(!ok_warp || fresh || top > kRescaleLog2)) break;
           // a failed wait ends the role here, for all of its warps alike; O^T of the
           // tile before is complete from here on
           ok_warp = __all_sync(0xFFFFFFFFu, wait(&sm.p_free, (i & 1) ^ 1)) && ok_warp;
-          if (softmax_sync_or(!ok_warp)) return false;
+          if (softmax_sync_or<COLS>(!ok_warp)) return false;
           tc_fence_after();
           // the columns' maxima, from S once more: 16 columns at a time keep the code of
           // what happens once or twice in a segment small
 #pragma unroll 1
-          for (int c0 = 0; c0 < COLS; c0 += 16) {
+          for (int c0 = 0; c0 < kCols; c0 += 16) {
             float2 y[8];
             tmem_ld16_pairs(ts + c0, y);
             tmem_ld_wait();
@@ -1140,9 +1168,9 @@ struct Softmax {
             for (int k = 0; k < 16; ++k)
               if (c0 + k < clo || c0 + k >= chi) t[k] = -INFINITY;
             const float top16 = warp_reduce_many<16, true>(t, lane);
-            if ((lane & 1) == 0) sm.red[warp][c0 + (lane >> 1)] = top16;
+            if ((lane & 1) == 0) sm.red[quarter][cb + c0 + (lane >> 1)] = top16;
           }
-          softmax_sync();
+          softmax_sync<COLS>();
           bool seen = false;
           if (tid < COLS) {                      // by how much the column's max moves
             const float t = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]), fmaxf(sm.red[2][tid], sm.red[3][tid]));
@@ -1155,20 +1183,20 @@ struct Softmax {
             if (lane == 0) sm.moved[warp] = m;
           }
           const bool was_fresh = fresh;
-          fresh = !softmax_sync_or(seen) && fresh;   // the new maxima are visible
+          fresh = !softmax_sync_or<COLS>(seen) && fresh;   // the new maxima are visible
           moved = true;
           if (was_fresh) continue;
 #pragma unroll
-          for (int k = 0; k < COLS; k += 4) {
+          for (int k = 0; k < kCols; k += 4) {
             const float4 f = al[k / 4];
             lpart[k / 2] = make_float2(lpart[k / 2].x * f.x, lpart[k / 2].y * f.y);
             lpart[k / 2 + 1] = make_float2(lpart[k / 2 + 1].x * f.z, lpart[k / 2 + 1].y * f.w);
           }
 #pragma unroll 1
-          for (int j = 0; j < 2 * (COLS / 16); ++j) {   // 16 columns of two chunks
+          for (int j = 0; j < 2 * (kCols / 16); ++j) {   // 16 columns of two chunks
             const int c0 = 16 * (j >> 1);
-            if (!((sm.moved[c0 / 32] >> (c0 & 31)) & 0xFFFFu)) continue;
-            const uint32_t ta = lane_off + 128 * (j & 1) + c0;
+            if (!((sm.moved[(cb + c0) / 32] >> ((cb + c0) & 31)) & 0xFFFFu)) continue;
+            const uint32_t ta = lane_off + 128 * (j & 1) + cb + c0;
             float2 v[2][8];
             tmem_ld16_pairs(ta, v[0]);
             tmem_ld16_pairs(ta + 64, v[1]);
@@ -1193,9 +1221,9 @@ struct Softmax {
         }
         tc_fence_before();
         warp_arrive(&sm.s_free[i & 1], lane);
-        uint32_t packed[COLS / 2];
+        uint32_t packed[kCols / 2];
 #pragma unroll
-        for (int k = 0; k < COLS / 2; ++k) {
+        for (int k = 0; k < kCols / 2; ++k) {
           float2 p = make_float2(ex2(x[k].x), ex2(x[k].y));
           lpart[k] = add2(lpart[k], p);
           if (!plain) p = make_float2(p.x * fmaxf(mu, 0.0f), p.y * fmaxf(mu, 0.0f));
@@ -1208,8 +1236,8 @@ struct Softmax {
         __syncwarp();
         uint8_t* prow = sm.p + (mykey >> 3) * 1024;
 #pragma unroll
-        for (int k = 0; k < COLS / 8; ++k)
-          *reinterpret_cast<uint4*>(prow + swz128(mykey & 7, k)) =
+        for (int k = 0; k < kCols / 8; ++k)
+          *reinterpret_cast<uint4*>(prow + swz128(mykey & 7, cb / 8 + k)) =
               make_uint4(packed[4 * k], packed[4 * k + 1], packed[4 * k + 2], packed[4 * k + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
@@ -1217,14 +1245,14 @@ struct Softmax {
       }
       // ---- the columns' sums
 #pragma unroll
-      for (int n = 0; n < COLS; n += 16) {
+      for (int n = 0; n < kCols; n += 16) {
         float t[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) t[k] = (k & 1) ? lpart[(n + k) / 2].y : lpart[(n + k) / 2].x;
         const float sum = warp_reduce_many<16, false>(t, lane);
-        if ((lane & 1) == 0) sm.red[warp][n + (lane >> 1)] = sum;
+        if ((lane & 1) == 0) sm.red[quarter][cb + n + (lane >> 1)] = sum;
       }
-      softmax_sync();
+      softmax_sync<COLS>();
       if (tid < COLS) {
         const float l = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
         const float m = l == 0.0f ? kNoMax : -sm.neg_m[tid];
@@ -1238,7 +1266,7 @@ struct Softmax {
           }
         }
       }
-      softmax_sync();
+      softmax_sync<COLS>();
       prev_r0 = w.gr.r0;
       prev_cols = cols;
       prev_slot = slot;
@@ -1271,20 +1299,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_attn(const __grid_constan
       mbar_init(&sm.k_full[i], 4);
       mbar_init(&sm.k_free[i], 1);
       mbar_init(&sm.s_full[i], 2);
-      mbar_init(&sm.s_free[i], kSoftmaxWarps);
+      mbar_init(&sm.s_free[i], kSoftmaxUsed<COLS>);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sm.v_full[i], 4);
       mbar_init(&sm.v_free[i], 1);
     }
-    mbar_init(&sm.p_full, kSoftmaxWarps);
+    mbar_init(&sm.p_full, kSoftmaxUsed<COLS>);
     mbar_init(&sm.p_free, 1);
     mbar_init(&sm.q_raw, 32);
-    mbar_init(&sm.q_full, kSoftmaxWarps);
+    mbar_init(&sm.q_full, kSoftmaxUsed<COLS>);
     mbar_init(&sm.q_free, 1);
     mbar_init(&sm.o_full, 1);
-    mbar_init(&sm.o_free, kSoftmaxWarps);
+    mbar_init(&sm.o_free, kSoftmaxUsed<COLS>);
     mbar_init(&sm.drain, 2);
     fence_barrier_init();
     sm.abort = 0;
@@ -1298,20 +1326,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_attn(const __grid_constan
   __syncthreads();
   tc_fence_after();
   // all 512 columns are this CTA's, so they start at address 0
-  // registers: 512 x 128 at launch = 256 x 128 + 128 x 208 + 128 x 48
+  // registers: 640 x 96 at launch = 256 x 128 + 256 x 96 + 128 x 32
   if (warp < kDequantWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     Dequant<COLS> d{a, sm, lane, warp >> 2, lane & 3, 32 * (warp & 3) + (lane >> 2),
                     kTmemK + 64 * (warp >> 2) + ((uint32_t)(32 * (warp & 3)) << 16)};
     d.run(sh, G);
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int v = warp - kDequantWarps;
-    int4 rec = make_int4(-1, 0, 0, 0);
-    Softmax<COLS> s{a, sm, lane, v};
-    const bool ok = s.run(sh, G, rec);
-    if (v == 0 && lane == 0) a.rec[blockIdx.x] = ok ? rec : make_int4(-1, 0, 0, 0);
+    if (v < kSoftmaxUsed<COLS>) {
+      int4 rec = make_int4(-1, 0, 0, 0);
+      Softmax<COLS> s{a, sm, lane, v};
+      const bool ok = s.run(sh, G, rec);
+      if (v == 0 && lane == 0) a.rec[blockIdx.x] = ok ? rec : make_int4(-1, 0, 0, 0);
+    }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp < kMmaWarp + 2) {
       Issue<COLS> m{a, sm};
       if (warp == kMmaWarp) m.run_scores(sh, G);

@@ -1112,36 +1112,38 @@ struct Softmax {
         bool moved = false;
 #pragma unroll 1
         for (;;) {                               // again once the running max has moved
-          // x = logit - m; a column that does not see the key: -inf
+          if (!fresh || moved) {
+            // x = logit - m; a column that does not see the key: -inf
 #pragma unroll
-          for (int k = 0; k < kCols; k += 16) tmem_ld16_pairs(ts + k, &x[k / 2]);
-          tmem_ld_wait();
+            for (int k = 0; k < kCols; k += 16) tmem_ld16_pairs(ts + k, &x[k / 2]);
+            tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < kCols / 2; ++k) asm volatile("" : "+f"(x[k].x), "+f"(x[k].y));   // not before the wait
-          if (!plain) {
+            for (int k = 0; k < kCols / 2; ++k) asm volatile("" : "+f"(x[k].x), "+f"(x[k].y));   // not before the wait
+            if (!plain) {
 #pragma unroll
-            for (int k = 0; k < kCols / 2; ++k) x[k] = make_float2(x[k].x * mu, x[k].y * mu);
-          }
-#pragma unroll
-          for (int k = 0; k < kCols; k += 4) {
-            const float4 f = fac[k / 4], m = mr[k / 4];
-            x[k / 2] = fma2(x[k / 2], make_float2(f.x, f.y), make_float2(m.x, m.y));
-            x[k / 2 + 1] = fma2(x[k / 2 + 1], make_float2(f.z, f.w), make_float2(m.z, m.w));
-          }
-          if (!plain) {
-#pragma unroll
-            for (int k = 0; k < kCols; k += 2) {
-              if (k < clo || k >= chi) x[k / 2].x = -INFINITY;
-              if (k + 1 < clo || k + 1 >= chi) x[k / 2].y = -INFINITY;
+              for (int k = 0; k < kCols / 2; ++k) x[k] = make_float2(x[k].x * mu, x[k].y * mu);
             }
-          }
-          if (moved) break;
-          float top = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < kCols / 2; ++k) top = fmaxf(fmaxf(top, x[k].x), x[k].y);
-          // The running max moves only when a logit exceeds it by more than 2^14, or at
-          // the segment's first key; usually it stays, and then no max or sum is reduced.
-          if (!softmax_sync_or<COLS>(!ok_warp || fresh || top > kRescaleLog2)) break;
+            for (int k = 0; k < kCols; k += 4) {
+              const float4 f = fac[k / 4], m = mr[k / 4];
+              x[k / 2] = fma2(x[k / 2], make_float2(f.x, f.y), make_float2(m.x, m.y));
+              x[k / 2 + 1] = fma2(x[k / 2 + 1], make_float2(f.z, f.w), make_float2(m.z, m.w));
+            }
+            if (!plain) {
+#pragma unroll
+              for (int k = 0; k < kCols; k += 2) {
+                if (k < clo || k >= chi) x[k / 2].x = -INFINITY;
+                if (k + 1 < clo || k + 1 >= chi) x[k / 2].y = -INFINITY;
+              }
+            }
+            if (moved) break;
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kCols / 2; ++k) top = fmaxf(fmaxf(top, x[k].x), x[k].y);
+            // The running max moves only when a logit exceeds it by more than 2^14, or at
+            // the segment's first key; usually it stays, and then no max or sum is reduced.
+            if (!softmax_sync_or<COLS>(!ok_warp || top > kRescaleLog2)) break;
+          }
           // a failed wait ends the role here, for all of its warps alike; O^T of the
           // tile before is complete from here on
           ok_warp = __all_sync(0xFFFFFFFFu, wait(&sm.p_free, (i & 1) ^ 1)) && ok_warp;
@@ -1167,8 +1169,13 @@ struct Softmax {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
               if (c0 + k < clo || c0 + k >= chi) t[k] = -INFINITY;
-            const float top16 = warp_reduce_many<16, true>(t, lane);
-            if ((lane & 1) == 0) sm.red[quarter][cb + c0 + (lane >> 1)] = top16;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) t[k] = warp_top(t[k]);
+            if (lane == 0) {
+#pragma unroll
+              for (int k = 0; k < 16; k += 4)
+                *reinterpret_cast<float4*>(&sm.red[quarter][cb + c0 + k]) = make_float4(t[k], t[k + 1], t[k + 2], t[k + 3]);
+            }
           }
           softmax_sync<COLS>();
           bool seen = false;

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import fp4_sparse_attention_csa_gb300 as csa
-from dense_ref import Case
+from dense_ref import Case, row_reference
 
 gpu = pytest.mark.gpu
 
@@ -323,3 +323,66 @@ def test_wait_budget_runs_out_and_the_next_call_is_exact(H):
     c.out.fill_(7.0)
     c.call()
     assert csa.csa_check_device_status(c.ws) == (0, 0) and torch.equal(c.out, first)
+
+
+@gpu
+def test_two_calls_at_once_on_their_own_streams():
+    cases = []
+    for k, H in enumerate((64, 16)):
+        g = np.random.default_rng(20 + k)
+        ctx = [int(x) for x in g.integers(2, 9000, 48)]
+        c = Case(190 + k, ctx, 2, 128)
+        q = c.queries(48, H)
+        assert c.run(csa, list(range(48)), [x - 1 for x in ctx], H, q) == (0, 0)
+        cases.append((c, c.out.clone(), torch.cuda.Stream()))
+    for _ in range(5):
+        for c, _, s in cases:
+            c.out.fill_(7.0)
+            s.wait_stream(torch.cuda.current_stream())
+        for _ in range(4):
+            for c, _, s in cases:
+                c.call(s)
+        for c, first, s in cases:
+            torch.cuda.current_stream().wait_stream(s)
+            assert torch.equal(c.out, first)
+
+
+@gpu
+def test_pages_past_four_gigabytes():
+    c = Case(200, [3000, 77], 2, 128)
+    q = c.queries(2, 64)
+    assert c.run(csa, [0, 1], [2999, 76], 64, q) == (0, 0)
+    first = c.out.clone()
+    n = 240000                                            # pages of 18432 bytes
+    far = torch.zeros(n, 18432, dtype=torch.uint8, device="cuda")
+    far[n - c.num_pages:] = c.d_kv
+    table = torch.where(c.d_table >= 0, c.d_table + (n - c.num_pages), c.d_table)
+    # the index pool is not read: any one of enough pages
+    cache = csa.make_cache(far, far, table, n, 2)
+    c.out.fill_(7.0)
+    csa.csa_dense_attn(cache, c.window, c.rows, 64, c.d_q, 512 ** -0.5, c.out, c.lse, None, c.ws)
+    assert csa.csa_check_device_status(c.ws) == (0, 0) and torch.equal(c.out, first)
+
+
+@gpu
+def test_rows_past_four_gigabytes():
+    """66,000 rows of 64 heads: queries and outputs of 4.3 GB each."""
+    R = 66000
+    c = Case(210, [70, 300], 1, 0)
+    q = c.queries(2, 64)
+    assert c.run(csa, [0, 1], [69, 299], 64, q) == (0, 0)
+    c.d_req = (torch.arange(R, device="cuda") & 1).int()
+    c.d_pos = torch.where(c.d_req == 0, 69, 299).int()
+    rows = csa.make_rows(c.d_req, c.d_pos, 300, R // 2)
+    big = c.d_q.repeat(R // 2, 1, 1)
+    out = torch.full((R, 64, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(csa.csa_workspace_size(csa.OP_DENSE_ATTN, R, 300, 64), dtype=torch.uint8, device="cuda")
+    csa.csa_dense_attn(c.cache, None, rows, 64, big, 512 ** -0.5, out, None, None, ws)
+    assert csa.csa_check_device_status(ws) == (0, 0)
+    # every row within the formula's bound, as a group cut between CTAs sums its tiles
+    # in two parts and so need not give the bits of a whole one
+    for k, pos in ((0, 69), (1, 299)):
+        o, _, tol, _ = row_reference(c.kv, c.table[k], c.num_pages, 1, pos, q.double().numpy()[k], 512 ** -0.5, None, None)
+        o, tol = torch.from_numpy(o).cuda(), torch.from_numpy(np.broadcast_to(tol, o.shape).copy()).cuda()
+        for part in out[k::2].split(2000):
+            assert ((part.double() - o).abs() <= tol).all(), k

@@ -311,6 +311,17 @@ __device__ bool in_list(const int32_t* req, int n, int v) {
   return lo < n && __ldg(req + lo) == v;
 }
 
+// Adds a count to page p; false when the page has none.  By compare and swap, so that
+// nobody sees a count that is taken back.
+__device__ __forceinline__ bool add_count(int32_t* refs, int p) {
+  int seen = __ldcg(refs + p);
+  while (seen > 0) {                             // ends: each failure is another thread's success
+    const int was = atomicCAS(refs + p, seen, seen + 1);
+    if (was == seen) return true;
+    seen = was;
+  }
+  return false;
+}
 // Drops one count of page p; false when the page had none.
 __device__ __forceinline__ bool drop_count(int32_t* refs, int p) {
   if (atomicSub(refs + p, 1) > 0) return true;
@@ -376,8 +387,7 @@ __global__ void __launch_bounds__(256) k_pages_fork(PagesArgs a) {
       p = -1;
     }
     p = max(p, -1);
-    if (p >= 0 && atomicAdd(a.refs + p, 1) <= 0) {
-      atomicSub(a.refs + p, 1);
+    if (p >= 0 && !add_count(a.refs, p)) {
       flags |= CSA_FLAG_PAGE_OOB;
       p = -1;
     }

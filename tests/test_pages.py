@@ -456,3 +456,22 @@ def test_captured_step_reserves_appends_and_attends():
     for (a, la), (b, lb) in zip(run(True), run(False)):
         assert torch.equal(a, b) and torch.equal(la, lb)
         assert not torch.equal(a[0], a[2])      # the parent and the child attend with their own queries
+
+
+@gpu
+def test_every_child_of_a_slot_without_a_count_finds_it_empty():
+    """63 children share a parent one of whose pages has no count: none of them
+    takes it for another's, whatever their order."""
+    p = Pool(59, 64, 40, 200, [30] + [0] * 63)
+    lost = [int(x) for x in np.nonzero(p.m.refs == 0)[0][:10]]
+    p.table[0, 30:] = ints(lost)
+    table, refs = p.table.clone(), p.refs.clone()
+    p.m.table[1:, :30] = p.m.table[0, :30]
+    p.m.table[0, 30:] = lost
+    p.m.refs[p.m.table[0, :30]] += 63
+    for _ in range(30):
+        p.table.copy_(table)
+        p.refs.copy_(refs)
+        csa.csa_pages_fork(p.cache, p.pages, None, None, ints([0] * 63), ints(list(range(1, 64))), ints([40 * 64] * 63),
+                           p.ws)
+        p.check(csa.FLAG_PAGE_OOB)

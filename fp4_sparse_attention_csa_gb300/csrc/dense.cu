@@ -44,15 +44,16 @@
 // product's Q 510, values stored 1150, the rest 300) fills the port for 3500, and the
 // loads and stores queue behind the second product's, which lengthens the chain of
 // two tiles (convert, S, softmax, O^T, store) that one tile of space allows.  64 x 4096
-// queries over 4 long caches run at 750 TFLOP/s, 128 rows over 128 caches at 740, 0.40 of
+// queries over 4 caches of 8-16k run at 755 TFLOP/s, 128 rows over 128 caches at 748, 0.40 of
 // what cuBLAS reaches in bf16.  A step between groups costs about four tiles more
 // (queries in, first maximum, output); one token of 4096 is all such steps.
-// One kernel is 128 KB of code and the parts that run once per group are fetched
+// One kernel is 130 KB of code and the parts that run once per group are fetched
 // cold, at several clocks per instruction; loops there stay rolled.
 // Measured on the way (128 rows over 128 caches, us): one serial role per tile 868;
 // three roles, S from tensor memory 569; MMA loops rolled 488; entry tiles aligned to
 // pages, output by plain stores 485; the list of work with the steps' cost, cuts joined
-// in one wave 428; 8 softmax warps for 4: 419 (2 x 999 rows: 535, 580, 595, 435, 202, 187).
+// in one wave 428; 8 softmax warps for 4, the first tile straight to its maxima 414
+// (2 x 999 rows: 535, 580, 595, 435, 202, 182).
 #include <algorithm>
 
 #include "attn_device.cuh"

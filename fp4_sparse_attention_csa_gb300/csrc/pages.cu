@@ -17,10 +17,10 @@
 //
 // Measured on the device, with the two small copies that reset the tables, us:
 // forking 2 requests and reserving their next block 17; 64 x 3 children with a copied
-// page each 33 (32 MB both ways: the plan and the launches are half of it);
+// page each 34 (32 MB both ways: the plan and the launches are half of it);
 // releasing 96 requests and reserving 96 prompts 23; compacting 1500 pages 14, 49999
-// pages 112.  Of the last 91 are k_pages_move, 516 MB at 5.7 TB/s, 0.83 of a plain
-// copy's rate; the plan's 20 are two passes over the counts and their exchange.
+// pages 112.  Of the last 90 are k_pages_move, 516 MB at 5.7 TB/s, 0.84 of a plain
+// copy's rate, and 13 the plan: two passes over the counts and their exchange.
 #include <cooperative_groups.h>
 
 #include <algorithm>

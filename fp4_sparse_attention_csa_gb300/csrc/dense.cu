@@ -43,10 +43,10 @@
 // together.  A tile takes 5600: its shared-memory traffic (second product 1540, first
 // product's Q 510, values stored 1150, the rest 300) fills the port for 3500, and the
 // loads and stores queue behind the second product's, which lengthens the chain of
-// two tiles (convert, S, softmax, O^T, store) that one tile of space allows.  64 x 4096
-// queries over 4 caches of 8-16k run at 755 TFLOP/s, 128 rows over 128 caches at 748, 0.40 of
-// what cuBLAS reaches in bf16.  A step between groups costs about four tiles more
-// (queries in, first maximum, output); one token of 4096 is all such steps.
+// two tiles (convert, S, softmax, O^T, store) that one tile of space allows.  512
+// rows of 64 heads over 4 caches run at 755 TFLOP/s, 128 rows over 128 caches at 748,
+// 0.40 of what cuBLAS reaches in bf16.  A step between groups costs about four tiles
+// more (queries in, first maximum, output); one token of a short context is all step.
 // One kernel is 130 KB of code and the parts that run once per group are fetched
 // cold, at several clocks per instruction; loops there stay rolled.
 // Measured on the way (128 rows over 128 caches, us): one serial role per tile 868;
@@ -386,26 +386,14 @@ struct Walk {
 // and 2 wg + 1, 128 dims each.  Lane 4r + q holds rows r, r + 8, r + 16, r + 24, of
 // each chunk the 32 dims from 32 q (16 bytes: four words of 8 dims, two scales).
 // Four dims sit in two neighbouring columns of tensor memory; S sums over dims in
-// any order, and Q is laid out to match (q_place).  In shared memory lanes q >= 2
+// any order, and Q is laid out to match: dims d .. d + 3 (d a multiple of 4) of a chunk
+// are place d / 32, of four, in its 16-dim step (d / 4) % 8.  In shared memory lanes q >= 2
 // put word i where word i ^ 2 belongs, so that a quarter-warp's 16-byte stores hit
 // distinct banks; that permutes rows of O^T, and write_out undoes it.
 struct Raw {
   uint4 w[2][4];                                 // [chunk][row]
   uint16_t sc[2][4];                             // [chunk][row]: the lane's two scales
 };
-
-// Where the 4 dims from d (a multiple of 4) of a chunk sit: the 16-dim step of the
-// product and the place, of four, in it.
-__device__ __forceinline__ void q_place(int d, int& step, int& place) {
-  place = d >> 5;
-  step = (d >> 2) & 7;
-}
-
-__device__ __forceinline__ uint32_t ldg_nc_u32(const void* p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
 
 // Where a warp's 32 entries lie: half a page.  A warp with nothing to read (past the
 // last entry, or a page outside the pool) takes some page's codes, and scales of zero.
@@ -938,7 +926,7 @@ __device__ __forceinline__ void convert_queries(const DenseArgs& a, Smem<COLS>& 
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         if (first & 2) swap2(hi[u], hi[u + 2]);
-      const int place = (lane >> 1) & 3;         // as q_place has it for dims 16 (lane % 8) + 4 u; step 4 (lane % 2) + u
+      const int place = (lane >> 1) & 3;         // of dims 16 (lane % 8) + 4 u of a chunk; the step is 4 (lane % 2) + u
       uint8_t* dst = sm.q + (2 * (lane >> 3) + (lane & 1)) * (COLS * 128) + ((c + j) >> 3) * 1024 + 8 * (place & 1);
       if (!rope || lane < 28) {
 #pragma unroll
@@ -946,7 +934,7 @@ __device__ __forceinline__ void convert_queries(const DenseArgs& a, Smem<COLS>& 
           *reinterpret_cast<uint2*>(dst + swz128((c + j) & 7, 2 * (u ^ first) + (place >> 1))) = hi[u];
       }
       if (rope) {
-        // q_place of dims 64 + lane and 96 + lane of chunk 3: places 2 and 3 of a step
+        // dims 64 + lane and 96 + lane of chunk 3 are places 2 and 3 of a step
         const int at = (lane >> 4) * (COLS * 128) + ((c + j) >> 3) * 1024 +
                        swz128((c + j) & 7, 2 * ((lane >> 2) & 3) + 1) + 2 * (lane & 3);
 #pragma unroll

@@ -44,7 +44,7 @@
 // product's Q 510, values stored 1150, the rest 300) fills the port for 3500, and the
 // loads and stores queue behind the second product's, which lengthens the chain of
 // two tiles (convert, S, softmax, O^T, store) that one tile of space allows.  512
-// rows of 64 heads over 4 caches run at 755 TFLOP/s, 128 rows over 128 caches at 748,
+// rows of 64 heads over 4 caches run at 755 TFLOP/s, 128 rows over 128 caches at 776,
 // 0.40 of what cuBLAS reaches in bf16.  A step between groups costs about four tiles
 // more (queries in, first maximum, output); one token of a short context is all step.
 // One kernel is 130 KB of code and the parts that run once per group are fetched
@@ -52,8 +52,8 @@
 // Measured on the way (128 rows over 128 caches, us): one serial role per tile 868;
 // three roles, S from tensor memory 569; MMA loops rolled 488; entry tiles aligned to
 // pages, output by plain stores 485; the list of work with the steps' cost, cuts joined
-// in one wave 428; 8 softmax warps for 4, the first tile straight to its maxima 414
-// (2 x 999 rows: 535, 580, 595, 435, 202, 182).
+// in one wave 428; 8 softmax warps for 4, the first tile straight to its maxima 414;
+// a window's cost in the list 399 (2 x 999 rows: 535, 580, 595, 435, 202, 182, 177).
 #include <algorithm>
 
 #include "attn_device.cuh"
@@ -115,14 +115,17 @@ __device__ __forceinline__ Group group_at(const DenseArgs& a, int r, int G) {
   q.tiles = (q.Wp + q.n + kTileKeys - 1) / kTileKeys;
   return q;
 }
-// Units of work: a tile is one, and the step from one group to the next, which drains
-// the pipeline and fills it again, counts as kGap of them.  Without it a share of many
-// short groups takes far longer than one long group's: 2 x 999 rows of up to 8 tiles
-// took 391 us at 0, 218 at 2, 212 at 3, 214 at 4, 219 at 5; 128 rows of 24 to 260
-// tiles 473, 455, 452, 445, 433.  A group of no tiles takes one: its rows are
-// written out empty.
-constexpr int kGap = 4;
-__device__ __forceinline__ int group_units(const Group& q) { return q.tiles > 0 ? q.tiles + kGap : 1; }
+// Units of work: a tile is one; the step from one group to the next, which drains the
+// pipeline and fills it again, counts as kGap, and a window, whose tile is gathered from
+// the ring and converted twice, as kNear more.  Without them a share of many short
+// groups takes far longer than a part of one long one.  2 x 999 rows without a window,
+// up to 8 tiles each, and 128 rows of 17 to 513 tiles, us, by (kGap, kNear):
+// (0, 0) 391, 473; (4, 0) 182, 411; (3, 2) 177, 403; (3, 3) 177, 399; (2, 3) 179, 403.
+// A group of no tiles takes one unit: its rows are written out empty.
+constexpr int kGap = 3, kNear = 3;
+__device__ __forceinline__ int group_units(const Group& q) {
+  return q.tiles > 0 ? q.tiles + kGap + (q.W > 0 ? kNear : 0) : 1;
+}
 
 struct Share {
   int row, t0;                                   // the first group's row, and the share's first unit in it
@@ -199,7 +202,7 @@ __device__ __forceinline__ Share find_share(const DenseArgs& a, int G, ShareScra
     if (tid == kThreads - 1) s.total = upto;
     __syncthreads();
     const long long total = s.total;
-    per = (max(1ll, total - kGap) + gridDim.x - 1) / gridDim.x;   // nothing follows the last group
+    per = (max(1ll, total - kGap - kNear) + gridDim.x - 1) / gridDim.x;   // nothing follows the last group
     lo = min(total, (long long)blockIdx.x * per);
     units = (blockIdx.x + 1 == gridDim.x ? total : min(total, lo + per)) - lo;
     u = upto - sum;

@@ -45,7 +45,7 @@
 // loads and stores queue behind the second product's, which lengthens the chain of
 // two tiles (convert, S, softmax, O^T, store) that one tile of space allows.  512
 // rows of 64 heads over 4 caches run at 755 TFLOP/s, 128 rows over 128 caches at 776,
-// 0.40 of what cuBLAS reaches in bf16.  A step between groups costs about four tiles
+// 0.40 and 0.41 of what cuBLAS reaches in bf16.  A step between groups costs about three tiles
 // more (queries in, first maximum, output); one token of a short context is all step.
 // One kernel is 130 KB of code and the parts that run once per group are fetched
 // cold, at several clocks per instruction; loops there stay rolled.

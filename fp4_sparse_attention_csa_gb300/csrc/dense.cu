@@ -222,7 +222,10 @@ constexpr int kDequantWarps = 8, kSoftmaxWarps = 8;
 template <int COLS>
 constexpr int kSoftmaxUsed = COLS < 32 ? 4 : kSoftmaxWarps;
 constexpr int kMmaWarp = kDequantWarps + kSoftmaxWarps;
-constexpr float kNoMax = -3e38f;                 // running max of a column that has seen nothing
+// Running max of a column that has seen nothing: its first visible key's logit exceeds
+// it by far, so the key moves it like any other that does.  (With one max of 0 for all
+// such columns, one whose logits lie far below 0 lost its p to fp16.)
+constexpr float kNoMax = -3e38f;
 
 // Tensor memory columns: O^T chunk c at 64 c, S^T of even and odd tiles, and
 // the two chunks of K.
@@ -1048,7 +1051,7 @@ struct Softmax {
       if (more) {
         (void)wait(&sm.q_raw, segs++ & 1);       // one that runs out ends the role at S's wait
         convert_queries<COLS>(a, sm, w.gr, warp, lane);
-        if (tid < COLS) sm.neg_m[tid] = 0.0f;
+        if (tid < COLS) sm.neg_m[tid] = -kNoMax;
         fence_proxy_async_smem();
         warp_arrive(&sm.q_full, lane);
         softmax_sync<COLS>();                    // factors and maxima visible to all softmax warps
@@ -1065,7 +1068,7 @@ struct Softmax {
         prev_r0 = -1;
       }
       if (!more) break;
-      bool fresh = true;                         // no key of the segment seen yet: neg_m is not a max
+      bool fresh = true;                         // no column has seen a key of the segment yet
       // keys that every column sees (window keys aside); none when columns are unused
       const int all_see = cols == COLS ? w.gr.Wp + entries_at(a, w.gr.p0) : 0;
       float2 lpart[kCols / 2];                   // this key's share of the columns' sums of p
@@ -1132,8 +1135,8 @@ struct Softmax {
             float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kCols / 2; ++k) top = fmaxf(fmaxf(top, x[k].x), x[k].y);
-            // The running max moves only when a logit exceeds it by more than 2^14, or at
-            // the segment's first key; usually it stays, and then no max or sum is reduced.
+            // The running max moves only when a logit exceeds it by more than 14, or at the
+            // column's first key; usually it stays, and then no max or sum is reduced.
             if (!softmax_sync_or<COLS>(!ok_warp || top > kRescaleLog2)) break;
           }
           // a failed wait ends the role here, for all of its warps alike; O^T of the
@@ -1151,12 +1154,12 @@ struct Softmax {
             float t[16];
 #pragma unroll
             for (int k = 0; k < 16; k += 4) {
-              const float4 f = fac[(c0 + k) / 4], m = mr[(c0 + k) / 4];
+              const float4 f = fac[(c0 + k) / 4];
               asm volatile("" : "+f"(y[k / 2].x), "+f"(y[k / 2].y), "+f"(y[k / 2 + 1].x), "+f"(y[k / 2 + 1].y));
-              t[k] = fmaf(y[k / 2].x * mu, f.x, m.x);
-              t[k + 1] = fmaf(y[k / 2].y * mu, f.y, m.y);
-              t[k + 2] = fmaf(y[k / 2 + 1].x * mu, f.z, m.z);
-              t[k + 3] = fmaf(y[k / 2 + 1].y * mu, f.w, m.w);
+              t[k] = y[k / 2].x * mu * f.x;
+              t[k + 1] = y[k / 2].y * mu * f.y;
+              t[k + 2] = y[k / 2 + 1].x * mu * f.z;
+              t[k + 3] = y[k / 2 + 1].y * mu * f.w;
             }
 #pragma unroll
             for (int k = 0; k < 16; ++k)
@@ -1171,13 +1174,17 @@ struct Softmax {
           }
           softmax_sync<COLS>();
           bool seen = false;
-          if (tid < COLS) {                      // by how much the column's max moves
+          if (tid < COLS) {                      // the column's new max
             const float t = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]), fmaxf(sm.red[2][tid], sm.red[3][tid]));
             seen = t != -INFINITY;
-            // with one column every one that has grown moves, as the event is what costs
-            const float old = sm.neg_m[tid], now = old - ((fresh ? seen : t > 1.0f) ? t : 0.0f);
+            // with one column every one that has grown moves, as the event is what costs;
+            // one that had seen nothing takes its first max, whatever its sign, and has no
+            // sum or O to correct
+            const float old = sm.neg_m[tid];
+            const bool had = old != -kNoMax;
+            const float now = (had ? t + old > 1.0f : seen) ? -t : old;
             sm.neg_m[tid] = now;
-            sm.corr[tid] = fresh ? 1.0f : ex2(now - old);
+            sm.corr[tid] = had ? ex2(now - old) : 1.0f;
             const uint32_t m = __ballot_sync(COLS < 32 ? 0xFFFFu : 0xFFFFFFFFu, now != old);
             if (lane == 0) sm.moved[warp] = m;
           }

@@ -1,0 +1,83 @@
+"""csa_dense_attn where several rows of a request share their keys: a group's
+window fills two tiles there, and a share of the work may begin at the second."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_sparse_attention_csa_gb300 as csa
+from dense_ref import Case
+
+gpu = pytest.mark.gpu
+WIN, TILE = 128, 128
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    csa.build.build()
+    if torch.cuda.is_available():
+        torch.cuda.set_device(0)
+
+
+def rope_tables(rows, seed=5):
+    th = np.random.default_rng(seed).uniform(0, 2 * np.pi, (rows, 32))
+    return np.cos(th).astype(np.float32), np.sin(th).astype(np.float32)
+
+
+def shares_at_second_window_tile(ctx, r, H, P, sms):
+    """The first rows of the groups of whose tiles a CTA's share begins with the
+    second one, a window tile, and goes on to entries (the kernel's list of work)."""
+    cols = 16
+    while cols < 64 and cols < r * H:
+        cols *= 2
+    G = max(cols, H) // H
+    groups = []
+    for b, c in enumerate(ctx):
+        for k in range(0, r, G):
+            p0, g = c - r + k, min(G, r - k)
+            W = p0 + g - max(0, p0 - WIN + 1)
+            Wp = -(-W // TILE) * TILE
+            groups.append((b * r + k, Wp, -(-(Wp + (p0 + g) // P) // TILE)))
+    ends = np.cumsum([t + 6 for _, _, t in groups])
+    per = -(-(int(ends[-1]) - 6) // sms)
+    rows = []
+    for lo in range(0, int(ends[-1]), per):
+        i = int(np.searchsorted(ends, lo, side="right"))
+        r0, Wp, tiles = groups[i]
+        if lo - (int(ends[i]) - tiles - 6) == 1 and Wp == 2 * TILE and tiles > 2 and per > 1:
+            rows.append(r0)
+    return rows
+
+
+def common_block(c):
+    """Dims 0..15 of every key are 1."""
+    c.kv[:, (256 * np.arange(64)[:, None] + np.arange(8)).ravel()] = 0x22
+    c.kv[:, 16384 + 32 * np.arange(64)] = 0x38
+    c.wscale[:] = 2.0 ** -6
+    c.codes[..., :16] = 0x68
+
+
+@gpu
+@pytest.mark.parametrize("P", [1, 2])
+@pytest.mark.parametrize("H,r,B,rope", [(32, 2, 16, False), (32, 3, 16, False), (32, 128, 4, False), (16, 2, 16, False),
+                                        (16, 3, 16, False), (16, 4, 16, True), (16, 6, 16, False)])
+def test_logits_far_below_zero_where_a_share_begins_in_the_window(H, r, B, rope, P):
+    """Softmax does not see a shift of all logits, whatever tile a row meets first."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for more in range(0, 4096, 64):
+        ctx = [2050 * P + more + b for b in range(B)]
+        cut = shares_at_second_window_tile(ctx, r, H, P, sms)
+        if cut:
+            break
+    assert cut
+    c = Case(300 + H + r + P, ctx, P, WIN + r - 1)
+    common_block(c)
+    req = [b for b in range(B) for _ in range(r)]
+    pos = [p for b in range(B) for p in range(ctx[b] - r, ctx[b])]
+    tab = rope_tables(max(ctx)) if rope else None
+    scale = 512 ** -0.5
+    rows = sorted({row for r0 in cut[:4] for row in range(r0, min(r0 + 4, B * r))} | {0, B * r - 1})
+    for shift in (28, 60, 200):                           # log2 units
+        q = c.queries(B * r, H, 0.3)
+        q[..., :16] = -shift * np.log(2) / (16 * scale)
+        assert c.run(csa, req, pos, H, q, scale=scale, rope=tab) == (0, 0)
+        c.check(req, pos, H, q, scale=scale, rope=tab, rows=rows)

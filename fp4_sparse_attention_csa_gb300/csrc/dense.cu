@@ -13,7 +13,8 @@
 // values are the same fp16 tile, read K-major by the first product and MN-major
 // by the second.  Entries are exact in fp16 (e2m1 x E4M3); a window token is its
 // E4M3 codes times 2^e, e in [-14, 7], also exact, and the rest of its scale, mu,
-// multiplies its logits and p.  A query is scaled by a power of two so that its
+// multiplies its logits and p; rotated, e is at most 6, as a rotated pair may be sqrt(2)
+// times larger than its codes.  A query is scaled by a power of two so that its
 // largest element is in [128, 256), which undoes itself in the logit's factor.
 // A rotated query has more bits than fp16 holds: its last 64 dims are split into
 // fp16 high and low parts (22 bits), the low part four more steps of the first
@@ -67,11 +68,11 @@ constexpr int kThreads = 640;                    // 8 dequantising, 8 softmax, 2
 constexpr int kTileKeys = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// The running max moves when a logit exceeds it by this (log2 units): p <= 2^14,
-// times a window key's mu < 2, stays inside fp16, and a column rarely moves again
-// after its first tile (at 2^8 a column of widely spread logits still moved in
-// most early tiles).
-constexpr float kRescaleLog2 = 14.0f;
+// The running max moves when a logit exceeds it by this (log2 units): p <= 16159,
+// times a window key's mu < 4, stays inside fp16 (65504), and a column rarely moves
+// again after its first tile (at 8 a column of widely spread logits still moved in most
+// early tiles).
+constexpr float kRescaleLog2 = 13.98f;
 
 // ---- the list of work ----------------------------------------------------------------
 struct Group {
@@ -496,12 +497,15 @@ struct Dequant {
 
   // A chunk of a tile with window keys, for the first product (values: for the
   // second).  A window token is its codes times 2^e, e in [-14, 7] (exact); the rest
-  // of its scale is mu.  ki: the thread's first key.
+  // of its scale is mu, below 2 for scales up to 2^8.  448 * 2^7 fits fp16 and
+  // 448 * 2^7 * sqrt(2) does not, so with rotary tables e ends at 6 and mu below 4.
+  // ki: the thread's first key.
   __device__ __noinline__ static bool near_chunk(const DenseArgs& a, S& sm, bool values, int lane, int wg, int q,
                                                  int key0, uint32_t tslot, int h, uint32_t tile, int ki, int W,
                                                  int wlo, int b) {
     const int c = 2 * wg + h;
     const bool turn = c == 3 && q >= 2 && a.rope_cos != nullptr;
+    const int top = a.rope_cos ? 6 : 7;          // of all chunks: a token has one mu
     if (!values && c == 0 && lane == 0) sm.odd[tile & 1][key0 >> 5] = 1u;
     // the four rows' codes, before the wait
     uint4 u[4], v[4];
@@ -533,7 +537,7 @@ struct Dequant {
       for (int j = 0; j < 2; ++j) {
         const int k = ki + 8 * (s0 + j);
         const float scale = ws[s0 + j];
-        const int ex = scale > 0.0f ? min(7, max(-14, (int)(__float_as_uint(scale) >> 23) - 127)) : -14;
+        const int ex = scale > 0.0f ? min(top, max(-14, (int)(__float_as_uint(scale) >> 23) - 127)) : -14;
         const float pw = pow2(ex);
         if (turn && k < W) {
           const size_t row = (size_t)(wlo + k) * 32;

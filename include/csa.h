@@ -427,7 +427,7 @@ CSA_API csa_status_t csa_step_ex(const csa_cache_t* cache, const csa_window_t* w
  *  Rounding: P is rounded once to fp16 (11 bits), as are rotated window values;
  * rotated query values keep 22 bits, every other operand is exact, every sum and
  * the softmax are fp32.  A query vector may have any magnitude (it is scaled by a power of two);
- * window scales must stay below 2^8.
+ * window scales must stay below 2^8, and with rotary tables cos^2 + sin^2 below 2.
  *  q bf16 [R, H, 512]; out bf16 [R, H, 512]; lse fp32 [R, H] (nullable, natural
  * log).  n_heads 16, 32 or 64.  ws: csa_workspace_size(CSA_OP_DENSE_ATTN, R,
  * max_entries, n_heads) bytes, 256-byte aligned.  out must not overlap any

@@ -81,3 +81,43 @@ def test_logits_far_below_zero_where_a_share_begins_in_the_window(H, r, B, rope,
         q[..., :16] = -shift * np.log(2) / (16 * scale)
         assert c.run(csa, req, pos, H, q, scale=scale, rope=tab) == (0, 0)
         c.check(req, pos, H, q, scale=scale, rope=tab, rows=rows)
+
+
+@gpu
+@pytest.mark.parametrize("H,r", [(64, 1), (32, 2), (16, 4)])
+def test_rotated_window_tokens_at_the_largest_scales(H, r):
+    """Codes of 448 in both halves of a rotated pair under scales up to 2^8."""
+    ctx = [300, 131, 40]
+    c = Case(400 + H, ctx, 2, 140)
+    sign = c.g.integers(0, 2, (3, 140, 64), dtype=np.uint8) * 128
+    c.codes[..., 448:] = 0x7E + sign
+    c.wscale[:] = np.exp2(c.g.uniform(6, 7.999, c.wscale.shape))
+    c.wscale[0] = np.float32(255.99)
+    req = [b for b in range(3) for _ in range(r)]
+    pos = [p for b in range(3) for p in range(ctx[b] - r, ctx[b])]
+    q = c.queries(3 * r, H, 1e-4)
+    tab = rope_tables(300)
+    assert c.run(csa, req, pos, H, q, rope=tab) == (0, 0)
+    c.check(req, pos, H, q, rope=tab)
+
+
+@gpu
+@pytest.mark.parametrize("log2", [13.0, 13.97, 13.9999, 14.1])
+def test_weights_at_the_largest_step_of_the_maximum(log2):
+    """The second window tile's keys exceed the first's by as much as lets the
+    maximum stay, or a little more, under the largest window scale.  Enough
+    requests for both tiles to be one share's in most of them."""
+    B = 300
+    c = Case(420, [400] * B, 2, 140)
+    c.kv[:, 16384:] = 0                                   # entries of zeros
+    c.wscale[:] = np.float32(255.99)
+    c.codes[..., 0] = 0
+    c.codes[:, np.arange(397, 400) % 140, 0] = 0x68       # 64
+    c.codes[..., 448:] = 0x7E
+    q = torch.zeros(4 * B, 16, 512, dtype=torch.bfloat16)
+    q[..., 0] = 2.0 ** -6
+    scale = log2 * np.log(2) / (255.99 * 64 * 2.0 ** -6)
+    tab = rope_tables(400)
+    req, pos = [b for b in range(B) for _ in range(4)], [396, 397, 398, 399] * B
+    assert c.run(csa, req, pos, 16, q, scale=scale, rope=tab) == (0, 0)
+    c.check(req, pos, 16, q, scale=scale, rope=tab, rows=list(range(0, 4 * B, 23)) + [4 * B - 1])

@@ -537,8 +537,8 @@ struct Dequant {
       for (int j = 0; j < 2; ++j) {
         const int k = ki + 8 * (s0 + j);
         const float scale = ws[s0 + j];
-        const int ex = scale > 0.0f ? min(top, max(-14, (int)(__float_as_uint(scale) >> 23) - 127)) : -14;
-        const float pw = pow2(ex);
+        const int ex = min(top, max(-14, (int)((__float_as_uint(scale) >> 23) & 255u) - 127));
+        const float pw = copysignf(pow2(ex), scale);
         if (turn && k < W) {
           const size_t row = (size_t)(wlo + k) * 32;
           uint32_t t[16];
@@ -559,7 +559,12 @@ struct Dequant {
             o[j][2 * i + 1] = hmul2_u32(f[1], hp);
           }
         }
-        if (!values && c == 0 && q == 0) sm.mu[tile & 1][key0 + 8 * (s0 + j)] = k < W ? scale * pow2(-ex) : -1.0f;
+        if (!values && c == 0 && q == 0) {
+          // an infinite scale gives NaN, like NaN itself: the rows that see the token become
+          // NaN, and P is 0 in the others, which an infinite mu would turn into NaN as well
+          const float mu = fabsf(scale) * pow2(-ex);
+          sm.mu[tile & 1][key0 + 8 * (s0 + j)] = k < W ? fmaf(mu, 0.0f, mu) : -1.0f;
+        }
       }
       __syncwarp();
       if (!values) {
@@ -1092,7 +1097,7 @@ struct Softmax {
         if (!plain) {
           if (sm.odd[i & 1][quarter]) mu = sm.mu[i & 1][mykey];
           int ilo = 0, ihi = -1;                 // rows of the group
-          if (mu >= 0.0f) {
+          if (!(mu < 0.0f)) {
             if (ki < w.gr.Wp) {
               ilo = max(0, w.gr.wlo + ki - w.gr.p0);
               ihi = min(w.gr.g - 1, w.gr.wlo + ki + (WIN - 1) - w.gr.p0);
@@ -1236,7 +1241,7 @@ struct Softmax {
         for (int k = 0; k < kCols / 2; ++k) {
           float2 p = make_float2(ex2(x[k].x), ex2(x[k].y));
           lpart[k] = add2(lpart[k], p);
-          if (!plain) p = make_float2(p.x * fmaxf(mu, 0.0f), p.y * fmaxf(mu, 0.0f));
+          if (!plain) p = make_float2(p.x * fmaxf(mu, 0.0f), p.y * fmaxf(mu, 0.0f));   // of NaN: 0
           const __half2 hv = __floats2half2_rn(p.x, p.y);
           packed[k] = *reinterpret_cast<const uint32_t*>(&hv);
         }

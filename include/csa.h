@@ -428,6 +428,9 @@ CSA_API csa_status_t csa_step_ex(const csa_cache_t* cache, const csa_window_t* w
  * rotated query values keep 22 bits, every other operand is exact, every sum and
  * the softmax are fp32.  A query vector may have any magnitude (it is scaled by a power of two);
  * window scales must stay below 2^8, and with rotary tables cos^2 + sin^2 below 2.
+ *  Codes and entries' scales must be numbers (csa_append writes no others); a
+ * window token whose fp32 scale is infinite or NaN gives NaN to the rows that see
+ * it, and to no others.
  *  q bf16 [R, H, 512]; out bf16 [R, H, 512]; lse fp32 [R, H] (nullable, natural
  * log).  n_heads 16, 32 or 64.  ws: csa_workspace_size(CSA_OP_DENSE_ATTN, R,
  * max_entries, n_heads) bytes, 256-byte aligned.  out must not overlap any

@@ -121,3 +121,34 @@ def test_weights_at_the_largest_step_of_the_maximum(log2):
     req, pos = [b for b in range(B) for _ in range(4)], [396, 397, 398, 399] * B
     assert c.run(csa, req, pos, 16, q, scale=scale, rope=tab) == (0, 0)
     c.check(req, pos, 16, q, scale=scale, rope=tab, rows=list(range(0, 4 * B, 23)) + [4 * B - 1])
+
+
+@gpu
+@pytest.mark.parametrize("H,r", [(32, 2), (16, 4)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_token_without_a_finite_scale_stays_with_the_rows_that_see_it(H, r, bad):
+    """The last of a request's new tokens has overflowed: the rows before it do not see it."""
+    ctx = [700, 40, 131]
+    c = Case(500 + H, ctx, 2, 140)
+    for b, n in enumerate(ctx):
+        c.wscale[b, (n - 1) % 140] = bad
+    req = [b for b in range(3) for _ in range(r)]
+    pos = [p for b in range(3) for p in range(ctx[b] - r, ctx[b])]
+    q = c.queries(3 * r, H)
+    assert c.run(csa, req, pos, H, q) == (0, 0)
+    last = [r - 1, 2 * r - 1, 3 * r - 1]
+    c.check(req, pos, H, q, rows=[i for i in range(3 * r) if i not in last])
+    assert c.out[last].isnan().all() and c.lse[last].isnan().all()
+
+
+@gpu
+@pytest.mark.parametrize("rope", [False, True])
+def test_negative_window_scales(rope):
+    """A token is its codes times its scale, whatever the scale's sign."""
+    c = Case(510, [500, 90], 2, 140)
+    c.wscale *= np.where(c.g.random(c.wscale.shape) < 0.5, np.float32(-1), np.float32(1))
+    req, pos = [0, 0, 1, 1], [498, 499, 88, 89]
+    q = c.queries(4, 32)
+    tab = rope_tables(500) if rope else None
+    assert c.run(csa, req, pos, 32, q, rope=tab) == (0, 0)
+    c.check(req, pos, 32, q, rope=tab)

@@ -180,14 +180,14 @@ __host__ __device__ inline ReserveWs reserve_ws(void* ws, int64_t units) {
 }
 
 // One unit = one logical page of one request of the list.  The table slot of
-// unit u, or -1 when the unit is not asked for; the flag says why not.
-__device__ __forceinline__ int64_t unit_slot(const PagesArgs& a, int u, int upr, uint32_t& flag) {
+// unit u, or -1 when the unit is not asked for; an impossible request adds its flag.
+__device__ __forceinline__ int64_t unit_slot(const PagesArgs& a, int u, int upr, uint32_t& flags) {
   const int i = u / upr, b = __ldg(a.req + i);
   if (b < 0) return -1;
   const int64_t first = __ldg(a.arg0 + i), count = __ldg(a.arg1 + i);
   if (first < 0 || count < 0 || count > a.max_count ||
       (count > 0 && (first + count - 1) / PAGE >= a.max_pages)) {
-    flag = CSA_FLAG_ROW_INVALID;
+    flags |= CSA_FLAG_ROW_INVALID;
     return -1;
   }
   const int64_t lp = first / PAGE + u % upr;

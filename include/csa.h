@@ -479,8 +479,13 @@ CSA_API csa_status_t csa_pages_reserve(const csa_cache_t* cache, const csa_pages
  * releases the pages it held, then shares the parent's pages of entries 0 ..
  * entries[i] - 1 (no page is copied: csa_pages_reserve does that when one of them
  * writes), and the parent's window ring (window nullable) and pending token
- * (nullable) are copied.  child is the request list; a parent may have several
- * children, but none that is itself a child in the same call.  entries[i] < 0 or
+ * (nullable) are copied as they are, which is at the parent's end.  They are the
+ * child's too if it continues from there.  A child that continues from an earlier
+ * token finds its window in the copy only if it is at most capacity - 128 tokens
+ * back (later tokens have taken the others' slots), and the pending token is not
+ * its own.  The call cannot see either: pass NULL for what does not hold, and
+ * fill the child's window and pending token otherwise.  child is the request
+ * list; a parent may have several children, but none that is itself a child in the same call.  entries[i] < 0 or
  * past max_pages_per_req pages leaves that child as it was and raises
  * CSA_FLAG_ROW_INVALID.
  *  ws: 256 bytes or more for the status word, 256-byte aligned, or NULL (faults

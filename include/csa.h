@@ -450,8 +450,9 @@ CSA_API csa_status_t csa_dense_attn(const csa_cache_t* cache, const csa_window_t
  * that is not, or an id past num_requests, raises CSA_FLAG_ROW_INVALID and the
  * call changes nothing.  A table slot whose page id is past the pool, or whose
  * page has no count, raises CSA_FLAG_PAGE_OOB; csa_pages_reserve leaves it as it
- * is, the others empty it.  Results never depend on the order in which the
- * device works. */
+ * is, the others empty it.  While each page's count is at least the number of
+ * slots that name it, results do not depend on the order in which the device
+ * works. */
 typedef struct {
   int32_t* page_table;             /* the cache's page_table, writable            */
   int32_t* refs;                   /* [num_pages], 16-byte aligned                */

@@ -124,8 +124,9 @@ def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
-    # the handle alone: forming a Stream object takes 3 us of a call's 9
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # the handle alone, where torch offers it: forming a Stream object takes 3 us of a call's 9
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
 
 
 def _check(rc, where):

@@ -13,7 +13,7 @@ using namespace csa;
 
 namespace {
 
-// Budget of the index score's pipeline waits (csa_set_wait_budget).
+// Budget of the index score's and the dense attention's pipeline waits (csa_set_wait_budget).
 std::atomic<long long> g_wait_budget{kWaitBudget};
 
 // Device address of csa_index_score_noalloc's scratch array (end of file).

@@ -26,7 +26,7 @@
 // parts leave unnormalised O and (m, l) in the workspace (at most two per CTA),
 // and k_dense_merge joins them in CTA order.
 //
-// Pipeline.  One CTA per SM, three roles that meet only at mbarriers:
+// Pipeline.  One CTA per SM, roles that meet only at mbarriers:
 //   8 dequantising warps (two warpgroups, two 128-dim chunks of a tile each),
 //   8 softmax warps (32 keys x half of the columns each), also queries and output,
 //   2 warps that issue the MMAs, one for each product, one that prefetches entries
@@ -122,6 +122,8 @@ __device__ __forceinline__ Group group_at(const DenseArgs& a, int r, int G) {
 // groups takes far longer than a part of one long one.  2 x 999 rows without a window,
 // up to 8 tiles each, and 128 rows of 17 to 513 tiles, us, by (kGap, kNear):
 // (0, 0) 391, 473; (4, 0) 182, 411; (3, 2) 177, 403; (3, 3) 177, 399; (2, 3) 179, 403.
+// Both are calls of 64 columns without rotary tables; 16 and 32 columns, and rotated
+// windows, which take longer, use the same two numbers.
 // A group of no tiles takes one unit: its rows are written out empty.
 constexpr int kGap = 3, kNear = 3;
 __device__ __forceinline__ int group_units(const Group& q) {
@@ -1387,7 +1389,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_attn(const __grid_constan
 // column (a CTA for every cut and column spent most of its time on being launched and
 // finding nothing to do).  Thread = 4 dims.  A cut of few parts is the work of a
 // quarter of a CTA, which needs no barrier; of one of many parts each quarter sums
-// every fourth, and the four sums are joined in a fixed order.  130 parts of 64
+// every fourth, and the four sums are joined in a fixed order.  129 parts of 64
 // columns (17 MB) take about 9 us, 25 with a CTA for every cut and column; bound by
 // the trips to L2, eight parts in flight a thread.
 constexpr int kMergeSplit = 4, kMergeLoads = 8, kMergeThreads = 128 * kMergeSplit;

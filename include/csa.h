@@ -426,8 +426,11 @@ CSA_API csa_status_t csa_step_ex(const csa_cache_t* cache, const csa_window_t* w
  * and candidate_blocks must be unset (CSA_ERR_INVALID_ARGUMENT).
  *  Rounding: P is rounded once to fp16 (11 bits), as are rotated window values;
  * rotated query values keep 22 bits, every other operand is exact, every sum and
- * the softmax are fp32.  A query vector may have any magnitude (it is scaled by a power of two);
- * window scales must stay below 2^8, and with rotary tables cos^2 + sin^2 below 2.
+ * the softmax are fp32.  A query vector may have any magnitude (it is scaled by a
+ * power of two); elements below 2^-24 of its largest are rounded to a step of
+ * 2^-31 of it.  Window scales must stay below 2^8, and with rotary tables
+ * cos^2 + sin^2 below 2; a scale below 2^-28 costs its token bits of P (its
+ * contribution is then off by up to 2^-39 of its codes).
  *  Codes and entries' scales must be numbers (csa_append writes no others); a
  * window token whose fp32 scale is infinite or NaN gives NaN to the rows that see
  * it, and to no others.
@@ -485,10 +488,10 @@ CSA_API csa_status_t csa_pages_reserve(const csa_cache_t* cache, const csa_pages
  * token finds its window in the copy only if it is at most capacity - 128 tokens
  * back (later tokens have taken the others' slots), and the pending token is not
  * its own.  The call cannot see either: pass NULL for what does not hold, and
- * fill the child's window and pending token otherwise.  child is the request
- * list; a parent may have several children, but none that is itself a child in the same call.  entries[i] < 0 or
- * past max_pages_per_req pages leaves that child as it was and raises
- * CSA_FLAG_ROW_INVALID.
+ * fill the child's window and pending token otherwise.
+ *  child is the request list; a parent may have several children, but none that
+ * is itself a child in the same call.  entries[i] < 0 or past max_pages_per_req
+ * pages leaves that child as it was and raises CSA_FLAG_ROW_INVALID.
  *  ws: 256 bytes or more for the status word, 256-byte aligned, or NULL (faults
  * are then not reported). */
 CSA_API csa_status_t csa_pages_fork(const csa_cache_t* cache, const csa_pages_t* pages, const csa_window_t* window,
@@ -522,8 +525,8 @@ CSA_API csa_status_t csa_check_device_status(void* ws, cudaStream_t stream, uint
 
 /* csa_set_wait_budget -- failure detection (no counterpart in the pages).
  * Every wait of the index score's and the dense attention's pipelines (a copy
- * landing, an MMA completing, a buffer coming free) is bounded by this many SM clocks; a wait
- * that runs out stops the kernel, which raises CSA_FLAG_TIMEOUT in the status
+ * landing, an MMA completing, a buffer coming free) is bounded by this many SM
+ * clocks; a wait that runs out stops the kernel, which raises CSA_FLAG_TIMEOUT in the status
  * word, waits for the copies and tensor-core work it already issued, frees
  * its tensor memory and returns.  Process-wide; takes effect at the next
  * call's launch.  sm_clocks <= 0 restores the default (3e9 clocks, about 1.5

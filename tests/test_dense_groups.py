@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import fp4_sparse_attention_csa_gb300 as csa
-from dense_ref import Case
+from dense_ref import Case, e4m3
 
 gpu = pytest.mark.gpu
 WIN, TILE = 128, 128
@@ -25,7 +25,8 @@ def rope_tables(rows, seed=5):
 
 def shares_at_second_window_tile(ctx, r, H, P, sms):
     """The first rows of the groups of whose tiles a CTA's share begins with the
-    second one, a window tile, and goes on to entries (the kernel's list of work)."""
+    second one, a window tile, and goes on to entries (the kernel's list of work:
+    a group with a window costs its tiles and 6 units, which the last one saves)."""
     cols = 16
     while cols < 64 and cols < r * H:
         cols *= 2
@@ -152,3 +153,28 @@ def test_negative_window_scales(rope):
     tab = rope_tables(500) if rope else None
     assert c.run(csa, req, pos, 32, q, rope=tab) == (0, 0)
     c.check(req, pos, 32, q, rope=tab)
+
+
+@gpu
+def test_tiny_window_scales_lose_no_more_than_stated():
+    """Tokens alone (no entry yet) under scales of 2^-34: P is subnormal, and off
+    by half its step, 2^-25, times codes of 2^-14."""
+    c = Case(430, [1], 2, 128)
+    c.wscale[:] = np.float32(2.0 ** -34)
+    q = c.queries(1, 32)
+    assert c.run(csa, [0], [0], 32, q) == (0, 0)
+    want = e4m3(c.codes[0, 0]) * 2.0 ** -34
+    err = np.abs(c.out[0].double().cpu().numpy() - want)
+    assert (err <= 2.0 ** -39 * np.abs(want) * 2.0 ** 34 + 2.0 ** -8 * np.abs(want)).all()
+
+
+@gpu
+def test_query_elements_far_below_the_largest():
+    """One element 2^16 times the others, against zeros in every key."""
+    c = Case(440, [900, 70], 1, 128)
+    c.kv[:, 256 * np.arange(64)] &= 0xF0
+    c.codes[..., 0] = 0
+    q = c.queries(2, 32)
+    q[..., 0] = 2.0 ** 16
+    assert c.run(csa, [0, 1], [899, 69], 32, q) == (0, 0)
+    c.check([0, 1], [899, 69], 32, q)

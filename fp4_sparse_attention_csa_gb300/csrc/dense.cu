@@ -1146,7 +1146,7 @@ struct Softmax {
             float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kCols / 2; ++k) top = fmaxf(fmaxf(top, x[k].x), x[k].y);
-            // The running max moves only when a logit exceeds it by more than 14, or at the
+            // The running max moves only when a logit exceeds it by kRescaleLog2, or at the
             // column's first key; usually it stays, and then no max or sum is reduced.
             if (!softmax_sync_or<COLS>(!ok_warp || top > kRescaleLog2)) break;
           }

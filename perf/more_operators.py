@@ -317,12 +317,12 @@ def plain_append(s):
     s["pool"][page, :, :side] = keys_in(key)
     s["pool"][page, :, side:2 * side] = values_in(code[:, :, 1].to(E4M3).view(torch.uint8))
     s["pool"][page, :, 2 * side:2 * side + 8] = scale.contiguous().view(torch.uint8)
-    # summary: the mean of the page's keys, summed as a binary tree over its 64 slots
-    mean = x[:, :, 0]
-    def pairs(y):
-        return y[:, :, 0::2] + y[:, :, 1::2]
-
-    mean = pairs(pairs(pairs(pairs(pairs(pairs(x[:, :, 0]))))))[:, :, 0] * (1 / BLOCK)
+    # summary: the mean of the page's keys, in a fixed order of sums
+    q = x[:, :, 0].unflatten(2, (4, 16))
+    part = q[..., 0, :] + q[..., 1, :]
+    for i in range(2, 16):
+        part = part + q[..., i, :]
+    mean = ((part[:, :, 0] + part[:, :, 1]) + (part[:, :, 2] + part[:, :, 3])) * (1 / BLOCK)
     top = mean.abs().amax(-1)
     inv = torch.where(top >= 2.0 ** -100, divided(127.0, top), 0.0)
     s["codes"][page] = (mean * inv[..., None]).round().clamp(-127, 127).to(torch.int8)

@@ -592,13 +592,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm<COLS, D>) k_kv8_attn(Kv8AttnA
 
 // ---- cut segments -----------------------------------------------------------------------------
 // A row of CTAs a cut, W warps a column; a warp sums its parts' O / l by their weights l 2^m, in the
-// parts' order.  Bound by latency: statistics and a warp's first 8 parts are asked for at once, 3.4 us
-// for the 33 parts of one token after 4096.
+// parts' order.  Weights count in 2^40: l grows with a part's keys, and O / l can be as large as a value.
+// Bound by latency: statistics and a warp's first 8 parts are asked for at once, 3.4 us for the 33 parts
+// of one token after 4096.
 constexpr int kMergeThreads = 512;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads, 2) k_kv8_merge(Kv8AttnArgs a, int cols_max) {
   constexpr int N = D / 32, kWarps = kMergeThreads / 32;
+  constexpr float kUnit = 9.094947017729282e-13f;            // 2^-40
   __shared__ float s_o[kWarps][D];
   const int warp = warp_id(), lane = lane_id();
   pdl_wait();
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) k_kv8_merge(Kv8AttnArgs a, i
           if (k0 == sub) {
             const float now = fmaxf(M, warp_top(m)), corr = ex2(M - now);
             M = now;
-            wgt = ex2(m - now) * l;
+            wgt = ex2(m - now) * l * kUnit;
             L = fmaf(L, corr, wgt);
 #pragma unroll
             for (int j = 0; j < N; ++j) acc[j] *= corr;
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) k_kv8_merge(Kv8AttnArgs a, i
       uint16_t* dst = a.out + row * D + N * lane;
       if constexpr (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
       else *reinterpret_cast<uint32_t*>(dst) = o[0];
-      if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+      if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L * (1.0f / kUnit))) * kLn2;
     }
   }
 }

@@ -1,0 +1,108 @@
+"""Attention over the 8-bit cache with values at the end of the range, against 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_sparse_attention_csa_gb300 as csa
+from kv8_ref import PAGE, RING, Cache, Device, bf16, dev, head_entries
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    csa.build.build()
+    if torch.cuda.is_available():
+        torch.cuda.set_device(0)
+
+
+def attend(pool, table_row, h, d, pos, q, scale, pages=None):
+    """(out [G, d], lse [G], bounds of both) of one row and key head in float64, q [G, d].
+
+    The bounds are those of the roundings that the calls state.  A query above 2^-9 of its largest element is exact,
+    below that 2^-17 of the largest is lost; a product's fp32 sums 2^-18 of the sum of magnitudes; a logit's factors
+    and its difference to a maximum 2^-21 of it and 2^-23 of the column's largest; powers of two, their sum and its
+    logarithm 2^-20 + n 2^-31.  A probability times its value's scale is kept to 2^-11 of itself and 2^-24 of the
+    row's largest such product, to which a page of no values adds nothing.  The output's sums 2^-18, its rounding to bf16
+    2^-8 and, of what bf16 no longer holds, half of its smallest step."""
+    pages = np.arange(pos // PAGE + 1) if pages is None else np.asarray(pages)
+    see = (pages[:, None] * PAGE + np.arange(PAGE)).reshape(-1) <= pos
+    k, v, sc = head_entries(pool, table_row, h, d, pages)
+    k, v, sv = k[see], v[see], np.repeat(sc[:, 1], PAGE)[see]
+    q = np.asarray(q, np.float64)
+    x = (q @ k.T) * scale
+    m = x.max(-1, keepdims=True)
+    p = np.exp(x - m)
+    L = p.sum(-1, keepdims=True)
+    lse, w = (m + np.log(L))[:, 0], p / L
+    out = w @ v
+    top = np.abs(q).max(-1, keepdims=True)
+    lost = 2.0 ** -17 * top * (np.abs(q) < 2.0 ** -9 * top)
+    dx = abs(scale) * (lost @ np.abs(k).T + 2.0 ** -18 * (np.abs(q) @ np.abs(k).T)) + 2.0 ** -21 * np.abs(x)
+    dx = dx.max(-1) + 2.0 ** -23 * np.abs(m[:, 0])
+    dl = dx + 2.0 ** -20 + len(k) * 2.0 ** -31 + 2.0 ** -22 * np.abs(lse)
+    code = np.abs(v) / np.where(sv > 0, sv, 1.0)[:, None]                 # zeros in a page of no values
+    do = (2.0 ** -11 + 2.0 ** -18 + 2 * dl[:, None]) * (w @ np.abs(v)) + 2.0 ** -24 * (w * sv).max(-1, keepdims=True) * code.sum(0)
+    return out, lse, do + 2.0 ** -8 * (np.abs(out) + do) + 2.0 ** -134, dl
+
+
+def check(s, req, pos, q, out, lse, rows=None, lists=None):
+    d, H = s.c.d, s.c.H
+    G = q.shape[1] // H
+    pool, table = s.pool.cpu().numpy(), s.table.cpu().numpy()
+    assert s.flags == (0, 0)
+    for r in range(len(req)) if rows is None else rows:
+        for h in range(H):
+            at = slice(h * G, h * G + G)
+            pages = None if lists is None else [j for j in lists[r][h] if j >= 0]
+            o, z, do, dz = attend(pool, table[req[r]], h, d, pos[r], bf16(q[r, at]), d ** -0.5, pages)
+            assert np.isfinite(out[r, at]).all() and np.isfinite(lse[r, at]).all(), (r, h, pos[r])
+            worst = np.abs(out[r, at] - o) / do
+            assert (worst <= 1).all(), (r, h, pos[r], float(worst.max()), float(np.abs(o).max()))
+            assert (np.abs(lse[r, at] - z) <= dz).all(), (r, h, lse[r, at] - z, dz)
+
+
+def keys_and_values(seed, n, kv, d, scales, climbs=None):
+    """n tokens; page j's values about scales[j] (0: none), its keys' first element climbs[j]."""
+    rng = np.random.default_rng(seed)
+    pages = -(-n // PAGE)
+    at = np.arange(n) // PAGE
+    k = rng.standard_normal((n, kv, d)) * 0.05
+    k[..., 0] = 0 if climbs is None else np.resize(climbs, pages)[at][:, None]
+    v = (rng.standard_normal((n, kv, d)) * 0.25 + 1) * np.resize(scales, pages)[at][:, None, None]
+    return bf16(k), bf16(v)
+
+
+def queries(rng, rows, kv, G, d):
+    """Columns that go along with the keys' first element, against it, or hardly look at it."""
+    q = bf16(rng.standard_normal((rows, kv * G, d)) * 0.5)
+    q[..., 0] = np.resize([8.0, -8.0, 0.25, 8.0, 2.0], kv * G)
+    return q
+
+
+def long_row(n, kv, d, scales, climbs, rows, G):
+    """One request's last rows, its cache filled on the GPU."""
+    k, v = keys_and_values(n, n, kv, d, scales, climbs)
+    c = Cache(n + G, [n], kv, d, tokens=[(np.zeros((0, kv, d), np.float32),) * 2])
+    s = Device.__new__(Device)
+    s.csa, s.c, s.rope = csa, c, None
+    s.pool = torch.zeros(c.pages, kv, 128 * d + 128, dtype=torch.uint8, device="cuda")
+    s.table, s.tail = dev(c.table), torch.zeros(1, kv, 2, RING, d, dtype=torch.bfloat16, device="cuda")
+    s.cache = csa.make_kv8(s.pool, s.tail, s.table, c.pages, kv, d)
+    csa.csa_kv8_append(s.cache, None, dev(np.zeros(1, np.int32)), dev(np.array([0, n], np.int32)), n, dev(k, torch.bfloat16),
+                       dev(v, torch.bfloat16))
+    torch.cuda.synchronize()
+    pos = list(range(n - rows, n))
+    q = queries(c.rng, rows, kv, G, d)
+    out, lse = s.attend([0] * rows, pos, q)
+    check(s, [0] * rows, pos, q, out, lse, sorted({0, rows - 1}))
+    return s, q, out, lse
+
+
+# ---- values near the end of the range -----------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("rows,G", [(1, 8), (1, 16), (1, 32), (20, 8)])
+@pytest.mark.parametrize("scale", [1e33, 6e37])
+def test_large_values_in_cut_rows(rows, G, scale):
+    """What parts add up to passes fp32's range unless their weights are small numbers."""
+    long_row(12000, 1, 128, [scale], [0.0], rows, G)

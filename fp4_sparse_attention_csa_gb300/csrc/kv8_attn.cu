@@ -14,7 +14,10 @@
 // is small against.  y = hi + mid / 16 + lo / 512 in E4M3 parts, to 2^-12 of itself and 2^-18
 // where the column's largest is at least 64: fp16's range, so that a long context's many small
 // probabilities are not lost beside a large one.  Each part has columns of its own in O.
-// The softmax's sum is l = sum of y / sv, in units of a power of two near 1 / sv.
+// The softmax's sum is l = sum of y / sv, in units of a power of two near 1 / sv.  That holds while a
+// segment's value scales lie within kKv8Near of its first tile's; from the first page on that does not,
+// the sum is formed with a maximum and powers of two of its own, l = sum of 2^(s - ms): y may have
+// none of a key that the sum is made of, and the other way round.
 // The key scale, the query's power of two and the softmax scale are the logit's factor.
 //
 // Work: the tiles of all segments, in row and head order, are one list; CTA i takes the i-th
@@ -76,6 +79,8 @@ struct Smem {
   int first_pos[X::kStages][2];                  // position of a page's first slot; INT_MAX: no page
   float factor[COLS];                            // of a column's logits (log2 units)
   float neg_m[COLS];                             // kTop minus the running maximum
+  float neg_l[COLS];                             // minus the sums' own maximum, once scales are far apart
+  int far;                                       // a page's scale is, in this tile
   float red[4][COLS];                            // per warp: maxima of a tile, sums of p
   float corr[COLS];                              // correction of a column whose maximum moved; at the end 1 / l
   int out_row[COLS];                             // a column's row of the output
@@ -286,28 +291,12 @@ __device__ __forceinline__ void convert_queries(const Kv8AttnArgs& a, Smem<COLS,
 
 // ---- softmax -------------------------------------------------------------------------------------
 template <int COLS, int D>
-struct Softmax {
-  using X = Shape<COLS, D>;
+struct Logits {
   static constexpr int CH = COLS < 16 ? COLS : 16;   // columns at a time
-  const Kv8AttnArgs& a;
   Smem<COLS, D>& sm;
   uint32_t tmem;                                 // with the warp's lanes
   int tid, warp, lane;
 
-  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-    return wait_or_abort(bar, parity, a.wait_budget, &sm.abort);
-  }
-  // tensor memory columns at + c0 .. (all lanes of the warp)
-  __device__ __forceinline__ void load_raw(uint32_t at, float (&v)[CH]) {
-    uint32_t t[16];
-    tmem_ld16(tmem + at, t);
-    tmem_ld_wait();
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      asm volatile("" : "+r"(t[k]));             // not before the wait
-      v[k] = __uint_as_float(t[k]);
-    }
-  }
   // S_hi + S_lo / 16 of columns c0 .. c0 + CH - 1
   __device__ __forceinline__ void load_scores(uint32_t at, int c0, float (&v)[CH]) {
     uint32_t t[16], u[16];
@@ -341,6 +330,89 @@ struct Softmax {
 #pragma unroll
       for (int k = 0; k < CH; ++k)
         if (c0 + k < clo) x[k] = -INFINITY;
+    }
+  }
+
+  // The tile's largest s + lsv of each column, the warps' to red; then a column's over all warps.
+  __device__ __forceinline__ void tile_tops(uint32_t at, float sk, float lsv, int clo, bool masked) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < COLS; c0 += CH) {
+      float y[CH];
+      logits(at, c0, sk, lsv, clo, masked, nullptr, y);
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const float t = warp_top(y[k]);
+        if (lane == 0) sm.red[warp][c0 + k] = t;
+      }
+    }
+    group_sync(1);
+  }
+  __device__ __forceinline__ float tile_top() {
+    return fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]), fmaxf(sm.red[2][tid], sm.red[3][tid]));
+  }
+};
+
+// l with this tile's keys, where sums have a maximum of their own.  units: of l, which so far counts from neg_m; -inf: it had
+// such a maximum before.  All threads of the four warps.  Seldom called, and kept out of the loop that calls it.
+template <int COLS, int D>
+__device__ __noinline__ void own_sum(Smem<COLS, D>& sm, uint32_t tmem, uint32_t at, float sk, int clo, float units, float* l) {
+  Logits<COLS, D> s{sm, tmem, (int)threadIdx.x, warp_id(), lane_id()};
+  constexpr int CH = Logits<COLS, D>::CH;
+  s.tile_tops(at, sk, 0.0f, clo, true);
+  if (s.tid < COLS) {
+    const float before = units == -INFINITY ? sm.neg_l[s.tid] : sm.neg_m[s.tid] + units, now = fminf(before, -s.tile_top());
+    sm.corr[s.tid] = ex2(now - before);
+    sm.neg_l[s.tid] = now;
+  }
+  group_sync(1);
+#pragma unroll 1
+  for (int c0 = 0; c0 < COLS; c0 += CH) {
+    float z[CH];
+    s.logits(at, c0, sk, 0.0f, clo, true, sm.neg_l, z);
+#pragma unroll
+    for (int k = 0; k < CH; ++k) l[c0 + k] = fmaf(l[c0 + k], sm.corr[c0 + k], ex2(z[k]));
+  }
+  group_sync(1);                                 // red and corr are the next maximum's
+}
+
+// O times neg_l, a factor by then.
+template <int COLS, int D>
+__device__ __noinline__ void scale_out(Smem<COLS, D>& sm, uint32_t tmem) {
+  using X = Shape<COLS, D>;
+#pragma unroll 1
+  for (int c0 = 0; c0 < X::kParts; c0 += 16) {
+    uint32_t u[16];
+    tmem_ld16(tmem + X::kOut + c0, u);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      asm volatile("" : "+r"(u[k]));             // not before the wait
+      u[k] = __float_as_uint(__uint_as_float(u[k]) * sm.neg_l[(c0 + k) % COLS]);
+    }
+    tmem_st16(tmem + X::kOut + c0, u);
+  }
+  tmem_st_wait();
+}
+
+template <int COLS, int D>
+struct Softmax : Logits<COLS, D> {
+  using X = Shape<COLS, D>;
+  using L = Logits<COLS, D>;
+  using L::CH, L::sm, L::tmem, L::tid, L::warp, L::lane, L::logits, L::tile_tops, L::tile_top;
+  const Kv8AttnArgs& a;
+
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    return wait_or_abort(bar, parity, a.wait_budget, &sm.abort);
+  }
+  // tensor memory columns at + c0 .. (all lanes of the warp)
+  __device__ __forceinline__ void load_raw(uint32_t at, float (&v)[CH]) {
+    uint32_t t[16];
+    tmem_ld16(tmem + at, t);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      asm volatile("" : "+r"(t[k]));             // not before the wait
+      v[k] = __uint_as_float(t[k]);
     }
   }
 
@@ -379,9 +451,7 @@ struct Softmax {
       for (; w.t < w.t_end; ++w.t, ++i) {
         const uint32_t st = i % X::kStages, at = (i % X::kScoreBufs) * 2 * COLS;
         ok = wait(&sm.full[st], (i / X::kStages) & 1) && ok;          // complete already: the scales are visible
-        ok = wait(&sm.s_full[i % X::kScoreBufs], (i / X::kScoreBufs) & 1) && ok;
-        tc_fence_after();
-        // the key, who sees it, and the pages' scales
+        // the key, who sees it, and the pages' scales, while S is on its way
         const int page = tid >> 6, base = sm.first_pos[st][page];
         const bool there[2] = {sm.first_pos[st][0] != INT_MAX, sm.first_pos[st][1] != INT_MAX};
         int clo = COLS;
@@ -389,18 +459,22 @@ struct Softmax {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float2 s = *reinterpret_cast<const float2*>(sm.stage[st] + 128 * D + k * X::kValueSlot + 64 * D);
-          if (!there[k]) continue;
           // a page of zero values has codes of zero: any scale will do, one like the others' is no maximum
-          if (s.y > 0.0f) near = log2f(s.y);
-          if (k == page) {
+          if (there[k] && s.y > 0.0f) near = log2f(s.y);
+          if (k != page) continue;
+          lsv = near;
+          if (there[k]) {
             sk = s.x;
-            lsv = near;
             clo = max(0, base + (tid & 63) - gr.p0) * a.G;
           }
         }
         if (w.t == w.t0) lref = rintf(near);
-        const float isv = ex2(lref - lsv);
+        // far from the first tile's: infinite, so that y is nothing to the sum and what any column sees moves the maximum
+        if (!(fabsf(lsv - lref) <= kKv8Near)) lsv = INFINITY;
+        float isv = ex2(lref - lsv);
         const bool masked = __any_sync(0xFFFFFFFFu, clo > 0);
+        ok = wait(&sm.s_full[i % X::kScoreBufs], (i / X::kScoreBufs) & 1) && ok;
+        tc_fence_after();
         float x[COLS];
         bool moved = w.t == w.t0;                // a segment's first tile goes straight to its maxima
         if (!moved) {
@@ -414,22 +488,25 @@ struct Softmax {
         if (group_sync_or(2, moved || !ok)) {
           // O of the tiles before is complete from here on
           ok = wait(&sm.p_free, (i & 1) ^ 1) && ok;
+          if (lsv == INFINITY) sm.far = 1;
           if (group_sync_or(2, !ok)) return false;
           tc_fence_after();
-#pragma unroll 1
-          for (int c0 = 0; c0 < COLS; c0 += CH) {
-            float y[CH];
-            logits(at, c0, sk, lsv, clo, masked, nullptr, y);
+          if (sm.far) {
+            float keep[COLS];
 #pragma unroll
-            for (int k = 0; k < CH; ++k) {
-              const float t = warp_top(y[k]);
-              if (lane == 0) sm.red[warp][c0 + k] = t;
-            }
+            for (int c = 0; c < COLS; ++c) keep[c] = l[c];
+            own_sum(sm, tmem, at, sk, clo, w.t > w.t0 ? lref : 0.0f, keep);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) l[c] = keep[c];
+            lref = -INFINITY;
+            isv = 0.0f;
+            const float own = *reinterpret_cast<const float*>(sm.stage[st] + 128 * D + page * X::kValueSlot + 64 * D + 4);
+            lsv = own > 0.0f ? log2f(own) : near;
           }
-          group_sync(1);
+          tile_tops(at, sk, lsv, clo, masked);
+          if (tid == 0) sm.far = 0;
           if (tid < COLS) {
-            const float t = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]), fmaxf(sm.red[2][tid], sm.red[3][tid]));
-            const float before = sm.neg_m[tid], now = fminf(before, kTop - t);
+            const float before = sm.neg_m[tid], now = fminf(before, kTop - tile_top());
             sm.corr[tid] = ex2(now - before);
             sm.neg_m[tid] = now;
           }
@@ -450,7 +527,7 @@ struct Softmax {
             tmem_st_wait();
           }
 #pragma unroll
-          for (int c = 0; c < COLS; ++c) l[c] *= sm.corr[c];
+          for (int c = 0; c < COLS; ++c) l[c] *= lref == -INFINITY ? 1.0f : sm.corr[c];
 #pragma unroll
           for (int c0 = 0; c0 < COLS; c0 += CH) logits(at, c0, sk, lsv, clo, masked, sm.neg_m, x + c0);
         } else {
@@ -504,8 +581,12 @@ struct Softmax {
       const int slot = w.t0 > 0 ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1;
       if (tid < COLS) {
         const float sum = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
-        const float m = -(sm.neg_m[tid] + lref);
-        sm.corr[tid] = sum == 0.0f ? 0.0f : pow2((int)lref) / sum;
+        // O counts in 2^-neg_m, l in 2^m
+        const bool far = lref == -INFINITY;
+        const float m = far ? -sm.neg_l[tid] : -(sm.neg_m[tid] + lref);
+        const float up = far ? ex2(-0.5f * (m + sm.neg_m[tid])) : pow2((int)lref);   // by halves: all of it may pass fp32's range
+        if (far) sm.neg_l[tid] = up;
+        sm.corr[tid] = sum == 0.0f ? 0.0f : up / sum;
         if (whole) {
           if (a.lse && tid < cols) a.lse[sm.out_row[tid]] = sum == 0.0f ? -INFINITY : (log2f(sum) + m) * kLn2;
         } else {
@@ -514,6 +595,7 @@ struct Softmax {
         }
       }
       group_sync(1);
+      if (lref == -INFINITY) scale_out(sm, tmem);
 #pragma unroll 1
       for (int c0 = 0; c0 < cols; c0 += CH) {
         float v[CH], mid[CH], lo[CH];
@@ -564,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<COLS, D>) k_kv8_attn(Kv8AttnA
     mbar_init(&sm.q_full, 4);
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.drain, 1);
-    sm.abort = 0;
+    sm.abort = sm.far = 0;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&sm.tmem_base, X::kTmem);
@@ -579,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<COLS, D>) k_kv8_attn(Kv8AttnA
     Products<COLS, D>{a, sm, tmem, false}.run(sh, RG);
   } else {
     int4 rec = make_int4(-1, 0, 0, 0);
-    Softmax<COLS, D> role{a, sm, tmem + ((uint32_t)(32 * warp) << 16), tid, warp, lane};
+    Softmax<COLS, D> role{{sm, tmem + ((uint32_t)(32 * warp) << 16), tid, warp, lane}, a};
     (void)role.run(sh, RG, rec);
     if (tid == 0) a.rec[blockIdx.x] = rec;
   }
@@ -592,7 +674,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<COLS, D>) k_kv8_attn(Kv8AttnA
 
 // ---- cut segments -----------------------------------------------------------------------------
 // A row of CTAs a cut, W warps a column; a warp sums its parts' O / l by their weights l 2^m, in the
-// parts' order.  Weights count in 2^40: l grows with a part's keys, and O / l can be as large as a value.
+// parts' order.  Weights count in 2^40: l grows with a part's keys, and O / l can be as large as a value.  Of their
+// sum's leading term, 2^-82 at least (kKv8Near), what fp32 drops is less than 2^-44.
 // Bound by latency: statistics and a warp's first 8 parts are asked for at once, 3.4 us for the 33 parts
 // of one token after 4096.
 constexpr int kMergeThreads = 512;

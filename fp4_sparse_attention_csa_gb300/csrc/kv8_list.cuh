@@ -216,6 +216,13 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return t0 == 0 && left >= gr.tiles; }
 };
 
+// ---- sums ----------------------------------------------------------------------------------
+// Value scales of a segment are near one another up to this many powers of two beside its first tile's.  There the
+// probabilities that the products take, y <= 2^15, serve the sum as well: the key that makes most of it has y >= 2^-90
+// (two scales can be 96 apart, and the largest y is 2^6 at least), and one that fp32 no longer holds, below 2^-126, is
+// 2^-36 of that at most.
+constexpr float kKv8Near = 48.0f;
+
 // ---- pages ---------------------------------------------------------------------------------
 // The pages of 16 tiles, one a lane: page number (INT_MAX: none) and pool page.
 struct Pages {

@@ -6,7 +6,9 @@
 // the first one's units: exact down to 2^-9 of the query's largest element, below that to 2^-17
 // of it); y = 2^(s + log2 sv - m) rounded once to fp16, at most 2^15 and at least 2^8 at the
 // column's largest; O += y V in fp16, V converted from E4M3 (exact).  Two threads have a column, one
-// with the keys of each page of a tile: their maximum, sum and correction need no other exchange.
+// with the keys of each page of a tile: their maximum, sum and correction need no other exchange.  Once a
+// segment's value scales are far apart, the sum has a maximum and powers of two of its own there, too; such
+// a tile's scales are infinite to the loop, so that it takes the way of a maximum that moves.
 //
 // Pipeline, one CTA per SM: 2 x 8 softmax warps (the halves' columns, a page of each tile each; two
 // warps that share columns meet once a tile, to agree whether the maximum moves), 4 warps that
@@ -62,6 +64,7 @@ struct Shape {
 // What the softmax needs of a tile besides S.
 struct Tile {
   float sk[2], lsv[2], isv[2];                   // key scale, log2 of the value scale, 2^lref over it
+  float own[2];                                  // log2 of the value scale where lsv is infinite: far from the segment's first
   float lref;                                    // units of the segment's sums
   int first[2];                                  // position of a page's first slot; INT_MAX: no page
 };
@@ -83,6 +86,7 @@ struct Smem {
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain;
   float2 joined[2][kHalf];                       // half b's -maximum and its pages' sums of a shared tile of columns
   float pair[2][2][kHalf];                       // [half][page]: what the two threads of a column tell one another
+  float own_top[2][2][kHalf], own_neg[2][2][kHalf];   // sums with a maximum of their own: a page's, minus the column's (NaN: not so)
   uint64_t b_full, b_free;                       // these and half b's O: complete, read
   uint32_t tmem_base;
   volatile int abort;                            // a wait ran out: every role leaves
@@ -100,6 +104,7 @@ __device__ __forceinline__ uint32_t f16x2_of(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ void group_pair_sync(int id) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 // ---- copies ------------------------------------------------------------------------------------
@@ -160,40 +165,44 @@ __device__ __forceinline__ void copy_side(const Kv8AttnArgs& a, Smem<D>& sm, con
 }
 
 // ---- scales and values ------------------------------------------------------------------------------
-// One warp: the tiles' scales as the softmax takes them.
+// One warp: the tiles' scales as the softmax takes them, a lane each page's.
 template <int D>
 __device__ __forceinline__ void prepare_scales(const Kv8AttnArgs& a, Smem<D>& sm, const Share& sh, int RG) {
   using X = Shape<D>;
+  const int lane = lane_id(), k = lane & 1;
   Walk w;
   uint32_t i = 0;
   float near = 0.0f, lref = 0.0f;                // log2 of the last value scale that is not 0
+  bool far = false;
   for (bool more = w.first(a, RG, sh); more && w.settle(a, RG); ++i, ++w.t) {
     const uint32_t st = i % X::kKeyStages;
     if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&sm.k_full[st], (i / X::kKeyStages) & 1, a.wait_budget, &sm.abort))) return;
-    Tile& t = sm.tile[i % X::kTiles];
-    if (w.t == w.t0) near = 0.0f;
-    float lsv[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float4 s = sm.scales[st][k];
-      const int first = sm.k_first[st][k];
-      // a page of zero values has codes of zero: any scale will do, one like the others' is no maximum
-      if (first != INT_MAX && s.y > 0.0f) near = log2f(s.y);
-      lsv[k] = near;
-      if (lane_id() == 0) {
-        t.sk[k] = first != INT_MAX ? s.x : 0.0f;
-        t.lsv[k] = near;
-        t.first[k] = first;
-      }
+    const float4 s = sm.scales[st][k];
+    const int first = sm.k_first[st][k];
+    if (w.t == w.t0) {
+      near = 0.0f;
+      far = false;
     }
+    // a page of zero values has codes of zero: any scale will do, one like the others' is no maximum
+    const bool some = first != INT_MAX && s.y > 0.0f;
+    const uint32_t which = __ballot_sync(0xFFFFFFFFu, some);
+    const float own = log2f(some ? s.y : 1.0f), own0 = __shfl_sync(0xFFFFFFFFu, own, 0), own1 = __shfl_sync(0xFFFFFFFFu, own, 1);
+    const float near0 = (which & 1u) ? own0 : near;
+    near = (which & 2u) ? own1 : near0;
+    const float lsv = k == 0 ? near0 : near;
     if (w.t == w.t0) lref = rintf(near);
-    if (lane_id() == 0) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) t.isv[k] = ex2(lref - lsv[k]);
+    far = far || __any_sync(0xFFFFFFFFu, !(fabsf(lsv - lref) <= kKv8Near));
+    Tile& t = sm.tile[i % X::kTiles];
+    if (lane < 2) {
+      t.sk[k] = first != INT_MAX ? s.x : 0.0f;
+      t.lsv[k] = far ? INFINITY : lsv;
+      t.isv[k] = far ? 0.0f : ex2(lref - lsv);
+      t.own[k] = lsv;
+      t.first[k] = first;
       t.lref = lref;
     }
-    warp_arrive(&sm.tile_full[i % X::kTiles], lane_id());
-    warp_arrive(&sm.k_free[st], lane_id());
+    warp_arrive(&sm.tile_full[i % X::kTiles], lane);
+    warp_arrive(&sm.k_free[st], lane);
   }
 }
 
@@ -428,6 +437,40 @@ __device__ __forceinline__ void convert_queries(const Kv8AttnArgs& a, Smem<D>& s
 }
 
 // ---- softmax ---------------------------------------------------------------------------------------
+// l of a column's page with this tile's keys, where sums have a maximum of their own.  own_neg is minus that, in units
+// of 2^lref as the probabilities' is, `neg` so far.  The two warps that share the columns meet once.  Seldom called, and
+// kept out of the loop that calls it.
+template <int D>
+__device__ __noinline__ float own_sum(Smem<D>& sm, uint32_t scores, int x, int p, int c, int seen, float fs, float neg, float lref, float l) {
+  float top = -INFINITY, sum = 0.0f, base = 0.0f;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass > 0) {
+      float before = sm.own_neg[x][p][c];
+      if (before != before) before = neg;
+      sm.own_top[x][p][c] = top;
+      group_pair_sync(1 + 4 * x + (c >> 5));
+      const float now = fminf(before, -fmaxf(sm.own_top[x][0][c], sm.own_top[x][1][c]) - lref);
+      sm.own_neg[x][p][c] = now;
+      base = now + lref;
+      l *= ex2(base - (before + lref));
+    }
+#pragma unroll 1
+    for (int k0 = 0; k0 < 64; k0 += 16) {
+      uint32_t u[16];
+      tmem_ld16(scores + k0, u);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        asm volatile("" : "+r"(u[k]));           // not before the wait
+        const float z = k0 + k < seen ? fmaf(__uint_as_float(u[k]), fs, base) : -INFINITY;
+        if (pass == 0) top = fmaxf(top, z);
+        else sum += ex2(z);
+      }
+    }
+  }
+  return l + sum;
+}
 template <int D>
 struct Softmax {
   using X = Shape<D>;
@@ -548,6 +591,7 @@ struct Softmax {
       const uint32_t n0 = n;
       const int tiles = w.t_end - w.t, step = joint ? 2 : 1;
       float neg = -kNoMax, l = 0.0f, lref = 0.0f;
+      sm.own_neg[x][p][c] = __int_as_float(0x7FFFFFFF);
 #pragma unroll 1
       for (int at = joint ? x : 0; at < tiles; at += step, ++n) {
         const uint32_t ti = i + at;
@@ -560,7 +604,8 @@ struct Softmax {
         const Tile& t = sm.tile[ti % X::kTiles];
         if (n == n0) lref = t.lref;
         const int first = t.first[p], seen = first == INT_MAX ? 0 : min(64, max(0, pos - first + 1));
-        const float fs = factor * t.sk[p], lsv = t.lsv[p], isv = t.isv[p];
+        const float fs = factor * t.sk[p], isv = t.isv[p];
+        float lsv = t.lsv[p];
         const bool masked = __any_sync(0xFFFFFFFFu, seen < 64);
         ok = wait(&sm.s_full[x], n & 1) && ok;
         tc_fence_after();
@@ -572,14 +617,17 @@ struct Softmax {
 #pragma unroll 1
         for (;;) {
           if (moves) {
+            const bool far = lsv == INFINITY;
+            if (far) lsv = t.own[p];
             sm.pair[x][p][c] = largest(seen, fs, lsv);
             ok = wait(&sm.pv_done[x], (n & 1) ^ 1) && ok;             // O of the tiles before is complete
             if (either(!ok)) return;
             tc_fence_after();
             const float top = fmaxf(sm.pair[x][0][c], sm.pair[x][1][c]);
             const float now = fminf(neg, kTop - top), corr = ex2(now - neg);
+            if (far) l = own_sum(sm, scores, x, p, c, seen, fs, neg, lref, l);   // the tile is here: both warps say so
+            else l *= corr;
             neg = now;
-            l *= corr;
             if (n > n0) {                        // a half of the dims each
 #pragma unroll 1
               for (int d = p * (D / 2); d < (p + 1) * (D / 2); d += 16) {
@@ -623,19 +671,30 @@ struct Softmax {
       sm.pair[x][p][c] = l;
       if (either(!ok)) return;
       l = sm.pair[x][0][c] + sm.pair[x][1][c];
+      float neg_l = sm.own_neg[x][p][c];
+      if (neg_l != neg_l) neg_l = neg;
       float own = 1.0f, others = 0.0f;           // weights of the halves' O
       if (joint) {
         const float2 b = sm.joined[0][c];
         const float lb = b.y + sm.joined[1][c].y, now = fminf(neg, b.x);
         own = ex2(now - neg);
         others = lb == 0.0f ? 0.0f : ex2(now - b.x);
-        l = lb == 0.0f ? l * own : fmaf(lb, others, l * own);
+        float nb = sm.own_neg[1][0][c];
+        if (nb != nb) nb = b.x;
+        const float least = fminf(neg_l, nb);
+        l *= ex2(least - neg_l);
+        if (lb != 0.0f) l = fmaf(lb, ex2(least - nb), l);
+        neg_l = least;
         neg = now;
       }
       const bool two = __any_sync(0xFFFFFFFFu, others != 0.0f);
       tc_fence_after();
       const int slot = w.t0 > 0 ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1;
-      const float m = -(neg + lref), f = l == 0.0f ? 0.0f : pow2((int)lref) / l;
+      // l and O count from neg_l and neg; by halves, as all of the difference may pass fp32's range
+      const float up = ex2(0.5f * (neg_l - neg));
+      own *= up;
+      others *= up;
+      const float m = -(neg_l + lref), f = l == 0.0f ? 0.0f : pow2((int)lref) * up / l;
       if (col < cols && p == 0) {
         if (whole) {
           const size_t row = (size_t)(gr.r0 + in_group) * a.heads * a.G + w.h * a.G + (col - in_group * a.G);

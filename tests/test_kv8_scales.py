@@ -1,4 +1,4 @@
-"""Attention over the 8-bit cache with values at the end of the range, against 64 bits."""
+"""Attention over pages of the 8-bit cache whose value scales lie far apart: outputs and sums against 64 bits, in groups of few and of many columns, whole rows and rows that are cut over the GPU."""
 import numpy as np
 import pytest
 import torch
@@ -80,6 +80,25 @@ def queries(rng, rows, kv, G, d):
     return q
 
 
+def bits(c, d):
+    """The first element of a key that puts a logit c powers of two above one of 0, for a query with 8 there."""
+    return c * np.log(2) * np.sqrt(d) / 8
+
+
+# rows and query heads a key head: 8, 16 and 32 columns; a tile of 128 columns shared by the halves; two tiles
+GROUPS = [(1, 4), (2, 8), (4, 7), (3, 16), (20, 8), (9, 33)]
+
+
+def run(seed, n, rows, G, d, scales, climbs, kv=1, lists=None):
+    c = Cache(seed, [n], kv, d, tokens=[keys_and_values(seed, n, kv, d, scales, climbs)])
+    s = Device(csa, c)
+    pos = list(range(n - rows, n))
+    q = queries(c.rng, rows, kv, G, d)
+    out, lse = s.attend([0] * rows, pos, q, lists)
+    check(s, [0] * rows, pos, q, out, lse, sorted({0, rows // 2, rows - 1}), lists)
+    return s, q, out, lse
+
+
 def long_row(n, kv, d, scales, climbs, rows, G):
     """One request's last rows, its cache filled on the GPU."""
     k, v = keys_and_values(n, n, kv, d, scales, climbs)
@@ -106,3 +125,31 @@ def long_row(n, kv, d, scales, climbs, rows, G):
 def test_large_values_in_cut_rows(rows, G, scale):
     """What parts add up to passes fp32's range unless their weights are small numbers."""
     long_row(12000, 1, 128, [scale], [0.0], rows, G)
+
+
+# ---- scales far apart -----------------------------------------------------------------------
+FAR = [[1e10, 1e-29], [1e30, 1e-15], [1e-25, 1e15], [1e-29, 1e37], [1e30, 1, 1e-20], [1e-20, 1, 1e30],
+       [1, 1, 1, 1e-18, 1, 1e18], [1e-9, 1e-9, 1e9, 1e-9]]
+
+
+@gpu
+@pytest.mark.parametrize("rows,G", GROUPS)
+@pytest.mark.parametrize("scales", FAR)
+def test_value_scales_far_apart(rows, G, scales):
+    """Flat logits, and pages of small values that some columns put far above the others, by up to 2^220."""
+    for d, n, climbs in ((128, 500, [0.0]), (64, 500, [0.0, bits(220, 64), bits(-60, 64)]), (64, 900, [bits(c, 64) for c in (3, -90, 110)])):
+        run(len(scales) + rows + n, n, rows, G, d, scales, climbs)
+
+
+@gpu
+@pytest.mark.parametrize("d,kv,rows,G", [(128, 1, 1, 8), (64, 2, 1, 16), (128, 1, 6, 16)])
+def test_value_scales_far_apart_in_cut_rows(d, kv, rows, G):
+    """A row's parts, in units of their own, joined; some parts' scales alike, some far apart."""
+    n = 12000
+    rng = np.random.default_rng(n + rows)
+    few = rng.choice([1e30, 1e-20, 1.0, 1e12], -(-n // PAGE), p=[0.02, 0.04, 0.9, 0.04])
+    far = 10.0 ** rng.integers(-28, 36, -(-n // PAGE))
+    for scales, climbs in ((few, [0.0]), (few, bits(rng.uniform(-70, 70, 188), d)), (far, bits(rng.uniform(-100, 100, 188), d))):
+        s, q, out, lse = long_row(n, kv, d, scales, climbs, rows, G)
+        again, lse2 = s.attend([0] * rows, list(range(n - rows, n)), q)
+        assert np.array_equal(out, again) and np.array_equal(lse, lse2)

@@ -15,9 +15,9 @@
 // where the column's largest is at least 64: fp16's range, so that a long context's many small
 // probabilities are not lost beside a large one.  Each part has columns of its own in O.
 // The softmax's sum is l = sum of y / sv, in units of a power of two near 1 / sv.  That holds while a
-// segment's value scales lie within kKv8Near of its first tile's; from the first page on that does not,
-// the sum is formed with a maximum and powers of two of its own, l = sum of 2^(s - ms): y may have
-// none of a key that the sum is made of, and the other way round.
+// segment's value scales lie within kKv8Near of its first tile's; from the first page on that does not, or
+// has no values at all (a scale of 0), the sum is formed with a maximum and powers of two of its own,
+// l = sum of 2^(s - ms): y may have none of a key that the sum is made of, and the other way round.
 // The key scale, the query's power of two and the softmax scale are the logit's factor.
 //
 // Work: the tiles of all segments, in row and head order, are one list; CTA i takes the i-th
@@ -445,30 +445,28 @@ struct Softmax : Logits<COLS, D> {
       float l[COLS];
 #pragma unroll
       for (int c = 0; c < COLS; ++c) l[c] = 0.0f;
-      float near = 0.0f;                         // log2 of the last value scale that is not 0
-      float lref = 0.0f;                         // about that of the segment's first tile, a whole number: l is in its units
+      float lref = 0.0f;                         // about log2 of the first tile's value scales, a whole number: l is in its units
 #pragma unroll 1
       for (; w.t < w.t_end; ++w.t, ++i) {
         const uint32_t st = i % X::kStages, at = (i % X::kScoreBufs) * 2 * COLS;
         ok = wait(&sm.full[st], (i / X::kStages) & 1) && ok;          // complete already: the scales are visible
         // the key, who sees it, and the pages' scales, while S is on its way
         const int page = tid >> 6, base = sm.first_pos[st][page];
-        const bool there[2] = {sm.first_pos[st][0] != INT_MAX, sm.first_pos[st][1] != INT_MAX};
-        int clo = COLS;
-        float sk = 0.0f, lsv = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 s = *reinterpret_cast<const float2*>(sm.stage[st] + 128 * D + k * X::kValueSlot + 64 * D);
-          // a page of zero values has codes of zero: any scale will do, one like the others' is no maximum
-          if (there[k] && s.y > 0.0f) near = log2f(s.y);
-          if (k != page) continue;
-          lsv = near;
-          if (there[k]) {
-            sk = s.x;
-            clo = max(0, base + (tid & 63) - gr.p0) * a.G;
-          }
+        auto scales = [&](int k) {
+          return *reinterpret_cast<const float2*>(sm.stage[st] + 128 * D + k * X::kValueSlot + 64 * D);
+        };
+        if (w.t == w.t0) {
+          const float sv[2] = {sm.first_pos[st][0] != INT_MAX ? scales(0).y : 0.0f, sm.first_pos[st][1] != INT_MAX ? scales(1).y : 0.0f};
+          lref = sv[1] > 0.0f ? rintf(log2f(sv[1])) : (sv[0] > 0.0f ? rintf(log2f(sv[0])) : 0.0f);
         }
-        if (w.t == w.t0) lref = rintf(near);
+        int clo = COLS;
+        float sk = 0.0f, lsv = lref;
+        if (base != INT_MAX) {
+          const float2 s = scales(page);
+          sk = s.x;
+          lsv = log2f(s.y);                      // -inf where there are no values: to the sum they count as others do
+          clo = max(0, base + (tid & 63) - gr.p0) * a.G;
+        }
         // far from the first tile's: infinite, so that y is nothing to the sum and what any column sees moves the maximum
         if (!(fabsf(lsv - lref) <= kKv8Near)) lsv = INFINITY;
         float isv = ex2(lref - lsv);
@@ -500,8 +498,7 @@ struct Softmax : Logits<COLS, D> {
             for (int c = 0; c < COLS; ++c) l[c] = keep[c];
             lref = -INFINITY;
             isv = 0.0f;
-            const float own = *reinterpret_cast<const float*>(sm.stage[st] + 128 * D + page * X::kValueSlot + 64 * D + 4);
-            lsv = own > 0.0f ? log2f(own) : near;
+            lsv = log2f(scales(page).y);         // of a page that is not there anything
           }
           tile_tops(at, sk, lsv, clo, masked);
           if (tid == 0) sm.far = 0;

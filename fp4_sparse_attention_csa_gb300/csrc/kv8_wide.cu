@@ -7,7 +7,7 @@
 // of it); y = 2^(s + log2 sv - m) rounded once to fp16, at most 2^15 and at least 2^8 at the
 // column's largest; O += y V in fp16, V converted from E4M3 (exact).  Two threads have a column, one
 // with the keys of each page of a tile: their maximum, sum and correction need no other exchange.  Once a
-// segment's value scales are far apart, the sum has a maximum and powers of two of its own there, too; such
+// segment's value scales are far apart, or 0, the sum has a maximum and powers of two of its own there, too; such
 // a tile's scales are infinite to the loop, so that it takes the way of a maximum that moves.
 //
 // Pipeline, one CTA per SM: 2 x 8 softmax warps (the halves' columns, a page of each tile each; two
@@ -172,25 +172,22 @@ __device__ __forceinline__ void prepare_scales(const Kv8AttnArgs& a, Smem<D>& sm
   const int lane = lane_id(), k = lane & 1;
   Walk w;
   uint32_t i = 0;
-  float near = 0.0f, lref = 0.0f;                // log2 of the last value scale that is not 0
+  float lref = 0.0f;
   bool far = false;
   for (bool more = w.first(a, RG, sh); more && w.settle(a, RG); ++i, ++w.t) {
     const uint32_t st = i % X::kKeyStages;
     if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&sm.k_full[st], (i / X::kKeyStages) & 1, a.wait_budget, &sm.abort))) return;
     const float4 s = sm.scales[st][k];
     const int first = sm.k_first[st][k];
+    const bool there = first != INT_MAX;
+    const float own = log2f(there ? s.y : 1.0f);   // -inf where there are no values: to the sum they count as others do
     if (w.t == w.t0) {
-      near = 0.0f;
+      const uint32_t some = __ballot_sync(0xFFFFFFFFu, there && s.y > 0.0f);
+      const float of0 = __shfl_sync(0xFFFFFFFFu, own, 0), of1 = __shfl_sync(0xFFFFFFFFu, own, 1);
+      lref = rintf((some & 2u) ? of1 : ((some & 1u) ? of0 : 0.0f));
       far = false;
     }
-    // a page of zero values has codes of zero: any scale will do, one like the others' is no maximum
-    const bool some = first != INT_MAX && s.y > 0.0f;
-    const uint32_t which = __ballot_sync(0xFFFFFFFFu, some);
-    const float own = log2f(some ? s.y : 1.0f), own0 = __shfl_sync(0xFFFFFFFFu, own, 0), own1 = __shfl_sync(0xFFFFFFFFu, own, 1);
-    const float near0 = (which & 1u) ? own0 : near;
-    near = (which & 2u) ? own1 : near0;
-    const float lsv = k == 0 ? near0 : near;
-    if (w.t == w.t0) lref = rintf(near);
+    const float lsv = there ? own : lref;
     far = far || __any_sync(0xFFFFFFFFu, !(fabsf(lsv - lref) <= kKv8Near));
     Tile& t = sm.tile[i % X::kTiles];
     if (lane < 2) {

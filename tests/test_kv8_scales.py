@@ -1,4 +1,5 @@
-"""Attention over pages of the 8-bit cache whose value scales lie far apart: outputs and sums against 64 bits, in groups of few and of many columns, whole rows and rows that are cut over the GPU."""
+"""Attention over pages of the 8-bit cache whose value scales lie far apart, or that hold no values at all: outputs and
+sums against 64 bits, in groups of few and of many columns, whole rows and rows that are cut over the GPU."""
 import numpy as np
 import pytest
 import torch
@@ -153,3 +154,44 @@ def test_value_scales_far_apart_in_cut_rows(d, kv, rows, G):
         s, q, out, lse = long_row(n, kv, d, scales, climbs, rows, G)
         again, lse2 = s.attend([0] * rows, list(range(n - rows, n)), q)
         assert np.array_equal(out, again) and np.array_equal(lse, lse2)
+
+
+# ---- pages of no values -----------------------------------------------------------------------
+NONE = [[0, 1e-3], [0, 1e-4, 1e-4], [0, 0, 1e-5], [0, 0, 0, 1e-20], [1, 0, 1, 1], [1e-3, 1e-3, 0, 0], [1.0, 0, 1e-20], [0, 1e30]]
+
+
+@gpu
+@pytest.mark.parametrize("rows,G", GROUPS)
+@pytest.mark.parametrize("scales", NONE)
+def test_pages_of_no_values(rows, G, scales):
+    """First in a row, in its first tile, in the middle and last; their keys as probable as others, or up to 2^150 more or
+    less so."""
+    for d, n, c in ((128, 500, 0), (64, 500, 7), (64, 700, 15), (128, 380, 150)):
+        run(len(scales) + rows + n, n, rows, G, d, scales, [bits(c, d) if x == 0 else 0.0 for x in scales])
+
+
+@gpu
+@pytest.mark.parametrize("rows,G", GROUPS)
+def test_rows_that_see_no_values_at_all(rows, G):
+    s, q, out, lse = run(rows + G, 300, rows, G, 64, [0.0], [0.0, 1.0])
+    assert not out.any()
+
+
+@gpu
+@pytest.mark.parametrize("d,kv,rows,G", [(128, 1, 1, 8), (64, 2, 1, 16), (128, 1, 6, 16)])
+def test_pages_of_no_values_in_cut_rows(d, kv, rows, G):
+    """Parts that begin with such pages, and some that have no others."""
+    n = 12000
+    rng = np.random.default_rng(n + rows)
+    scales = np.where(rng.random(188) < 0.4, 0.0, 1e-5)
+    scales[60:100] = 0
+    for climbs in (0 * scales, np.where(scales == 0, bits(9, d), 0.0), bits(rng.uniform(-20, 20, 188), d)):
+        long_row(n, kv, d, scales, climbs, rows, G)
+
+
+@gpu
+@pytest.mark.parametrize("rows,G", [(1, 4), (1, 16)])
+def test_listed_pages_of_no_values_and_far_scales(rows, G):
+    scales = [0, 1e-5, 1e10, 0, 1e-25, 1, 1]
+    run(3, 1200, rows, G, 64, scales, [bits(c, 64) for c in (5, 0, -60, 100, 80)], lists=[[[0, 3, 7, 8, 10, 11, 14]]])
+    run(4, 1200, rows, G, 64, scales, [0.0], lists=[[[1, 2, 4, 18]]])

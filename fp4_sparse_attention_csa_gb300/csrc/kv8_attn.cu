@@ -118,16 +118,16 @@ __device__ __forceinline__ void copy_pages(const Kv8AttnArgs& a, Smem<COLS, D>& 
     int chunk = -1;
     Pages x{INT_MAX, -1};
     if (a.blocks) {
-      while (chunk + 1 < w.t >> 4) x = pages_of(a, w.gr, w.h, ++chunk, above, ended);
+      while (chunk + 1 < w.t >> 4) x = pages_of<true>(a, w.gr, w.h, ++chunk, above, ended);
     } else {
       chunk = (w.t >> 4) - 1;
     }
-    Pages next = pages_of(a, w.gr, w.h, chunk + 1, above, ended);
+    Pages next = pages_of<true>(a, w.gr, w.h, chunk + 1, above, ended);
     for (; w.t < w.t_end; ++w.t, ++i) {
       if (w.t >> 4 != chunk) {
         chunk = w.t >> 4;
         x = next;
-        if (32 * (chunk + 1) < 2 * w.t_end) next = pages_of(a, w.gr, w.h, chunk + 1, above, ended);
+        if (32 * (chunk + 1) < 2 * w.t_end) next = pages_of<true>(a, w.gr, w.h, chunk + 1, above, ended);
       }
       const uint32_t st = i % X::kStages;
       ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&sm.free[st], ((i / X::kStages) & 1) ^ 1, a.wait_budget, &sm.abort));
@@ -156,6 +156,7 @@ __device__ __forceinline__ void copy_pages(const Kv8AttnArgs& a, Smem<COLS, D>& 
       }
       __syncwarp();
     }
+    if (w.t_end == w.gr.tiles) end_of_list(a, w.gr, w.h, ended);
   }
   // after a wait that ran out: what is still being copied must land before the CTA ends
   if (lane == 0)

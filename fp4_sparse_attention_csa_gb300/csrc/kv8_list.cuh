@@ -228,31 +228,72 @@ constexpr float kKv8Near = 48.0f;
 struct Pages {
   int j, page;
 };
-// Entries 32 chunk .. 32 chunk + 31 of a list, or those pages themselves.  `above` and `ended`
-// carry a list's rule from chunk to chunk.
+// A list of pages, 32 entries at a time by a whole warp.  An entry counts when it is one of the row's pages and above all
+// that count before it; those that count follow one another without gaps, so a row has no more of them than pages.
+// Which of entries i = 32 k + lane do: `above` is the largest that does before them, and becomes the largest so far;
+// `listed`, whether the entry stands before the list's end.
+__device__ __forceinline__ bool entry_counts(int e, bool listed, int last, int& above) {
+  const int lane = lane_id();
+  int top = listed && e <= last ? e : -1;         // the largest entry up to this lane
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, top, o);
+    if (lane >= o) top = max(top, y);
+  }
+  int before = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+  before = lane == 0 ? above : max(above, before);
+  above = max(above, __shfl_sync(0xFFFFFFFFu, top, 31));
+  return listed && e <= last && e > before;
+}
+// Those of tiles 16 chunk .. 16 chunk + 15, whatever the list holds: it is read from its beginning, and to its end
+// for the flag.
+__device__ __noinline__ inline int any_entries(const int32_t* list, int n_blocks, int last, int chunk, uint32_t* status) {
+  const int lane = lane_id();
+  int n = 0, above = -1, j = INT_MAX;            // n: how many count so far
+#pragma unroll 1
+  for (int i = 0; i < n_blocks; i += 32) {
+    const int e = i + lane < n_blocks ? __ldg(list + i + lane) : -1;
+    const uint32_t stop = __ballot_sync(0xFFFFFFFFu, e < 0);
+    const bool listed = lane < (stop ? __ffs(stop) - 1 : 32);
+    const uint32_t counts = __ballot_sync(0xFFFFFFFFu, entry_counts(e, listed, last, above));
+    if (listed && !((counts >> lane) & 1u)) raise_flag(status, CSA_FLAG_TOPK_OOB);
+    if ((n & 31) == 0 && (counts & (counts + 1)) == 0) {     // as they are
+      if (n == 32 * chunk && ((counts >> lane) & 1u)) j = e;
+      n += __popc(counts);
+    } else {
+#pragma unroll 1
+      for (uint32_t left = counts; left; left &= left - 1, ++n) {
+        const int v = __shfl_sync(0xFFFFFFFFu, e, __ffs(left) - 1);
+        if (n == 32 * chunk + lane) j = v;
+      }
+    }
+    if (stop) break;
+  }
+  return j;
+}
+// The pages of tiles 16 chunk .. 16 chunk + 15.  kCarry: `above` and `ended` carry a list's rule from chunk to chunk, and of
+// one with an entry that does not count nothing is above `above`; else a chunk is looked for by itself, which is less
+// code beside loops that have no lists.
+template <bool kCarry>
 __device__ __forceinline__ Pages pages_of(const Kv8AttnArgs& a, const Group& gr, int h, int chunk, int& above,
                                           bool& ended) {
   const int lane = lane_id(), i = 32 * chunk + lane, last = (gr.p0 + gr.g - 1) >> 6;
   Pages x{INT_MAX, -1};
   if (a.blocks == nullptr) {
     if (i <= last) x.j = i;
+  } else if (const int32_t* list = a.blocks + ((size_t)gr.r0 * a.heads + h) * a.n_blocks; !kCarry) {
+    x.j = any_entries(list, a.n_blocks, last, chunk, a.status);
   } else {
-    const int e = i < a.n_blocks && !ended ? __ldg(a.blocks + ((size_t)gr.r0 * a.heads + h) * a.n_blocks + i) : -1;
+    const int e = i < a.n_blocks && !ended ? __ldg(list + i) : -1;
     const uint32_t stop = __ballot_sync(0xFFFFFFFFu, e < 0);
     const bool listed = !ended && lane < (stop ? __ffs(stop) - 1 : 32);
     ended = ended || stop != 0;
-    int top = listed && e <= last ? e : -1;       // the largest entry up to this lane
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, top, o);
-      if (lane >= o) top = max(top, y);
-    }
-    int before = __shfl_up_sync(0xFFFFFFFFu, top, 1);
-    before = lane == 0 ? above : max(above, before);
-    above = max(above, __shfl_sync(0xFFFFFFFFu, top, 31));
-    if (listed) {
-      if (e <= last && e > before) x.j = e;
-      else raise_flag(a.status, CSA_FLAG_TOPK_OOB);
+    const bool counts = entry_counts(e, listed, last, above);
+    if (counts) x.j = e;
+    if (__any_sync(0xFFFFFFFFu, listed && !counts)) {
+      x.j = any_entries(list, a.n_blocks, last, chunk, a.status);
+      above = INT_MAX;
+      ended = false;
     }
   }
   if (x.j != INT_MAX) {
@@ -263,6 +304,11 @@ __device__ __forceinline__ Pages pages_of(const Kv8AttnArgs& a, const Group& gr,
     }
   }
   return x;
+}
+// Behind the segment's last tile: entries that no tile has are looked at, too (where kCarry, else they have been).
+__device__ __forceinline__ void end_of_list(const Kv8AttnArgs& a, const Group& gr, int h, bool ended) {
+  if (a.blocks == nullptr || ended || (gr.tiles + 15) / 16 * 32 >= a.n_blocks) return;
+  (void)any_entries(a.blocks + ((size_t)gr.r0 * a.heads + h) * a.n_blocks, a.n_blocks, (gr.p0 + gr.g - 1) >> 6, 0, a.status);
 }
 
 // ---- launch ------------------------------------------------------------------------------------

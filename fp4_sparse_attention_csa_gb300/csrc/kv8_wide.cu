@@ -121,15 +121,14 @@ __device__ __forceinline__ void copy_side(const Kv8AttnArgs& a, Smem<D>& sm, con
   bool ok = true;
   for (bool more = w.first(a, RG, sh); more && ok; more = w.next_segment(a, RG)) {
     if (w.t >= w.t_end) continue;
-    int above = -1, chunk = a.blocks ? -1 : (w.t >> 4) - 1;
+    int chunk = (w.t >> 4) - 1, above = -1;
     bool ended = false;
-    while (chunk + 1 < (w.t >> 4)) (void)pages_of(a, w.gr, w.h, ++chunk, above, ended);
-    Pages x{INT_MAX, -1}, next = pages_of(a, w.gr, w.h, chunk + 1, above, ended);
+    Pages x{INT_MAX, -1}, next = pages_of<false>(a, w.gr, w.h, chunk + 1, above, ended);
     for (; w.t < w.t_end; ++w.t, ++i) {
       if (w.t >> 4 != chunk) {
         chunk = w.t >> 4;
         x = next;
-        if (32 * (chunk + 1) < 2 * w.t_end) next = pages_of(a, w.gr, w.h, chunk + 1, above, ended);
+        if (32 * (chunk + 1) < 2 * w.t_end) next = pages_of<false>(a, w.gr, w.h, chunk + 1, above, ended);
       }
       const uint32_t st = i % kStages;
       ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&free[st], ((i / kStages) & 1) ^ 1, a.wait_budget, &sm.abort));

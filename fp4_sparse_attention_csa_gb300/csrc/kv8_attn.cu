@@ -781,7 +781,7 @@ template <int COLS, int D>
 cudaError_t launch_cols(Kv8AttnArgs a, int RG, uint8_t* ws, int num_sms, cudaStream_t stream) {
   static_assert(kPerSm<COLS, D> <= kMaxPerSm && kPerSm<COLS, D> * Shape<COLS, D>::kTmem <= 512, "tensor memory");
   static_assert(kPerSm<COLS, D> * (sizeof(Smem<COLS, D>) + 1024) <= 233472, "shared memory");
-  const int64_t pages = (a.rows.max_entries + PAGE - 1) / PAGE;
+  const int64_t pages = kv8_pages(a.rows.max_entries);
   const int grid = kv8_grid(a.rows.num_rows, a.heads, a.blocks ? std::min<int64_t>(pages, a.n_blocks) : pages,
                             num_sms * kPerSm<COLS, D>);
   kv8_place_parts(a, ws, grid, COLS);
@@ -816,7 +816,7 @@ cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, int cols, int grid, cudaStrea
 
 // For any split of the heads into groups and any number of pages up to max_entries'.
 size_t kv8_attn_ws_bytes(int32_t num_rows, int32_t max_entries, int32_t n_heads, int num_sms) {
-  const int64_t pages = (max_entries + PAGE - 1) / PAGE, most = (int64_t)num_rows * n_heads;
+  const int64_t pages = kv8_pages(max_entries), most = (int64_t)num_rows * n_heads;
   const int cols = group_cols(most) ? group_cols(most) : 32;
   const size_t narrow = kv8_parts_bytes(kv8_grid(num_rows, n_heads, pages, num_sms * kMaxPerSm), cols, 128);
   if (most <= 32) return narrow;

@@ -11,6 +11,8 @@ constexpr int kKv8Tail = CSA_KV8_TAIL;
 constexpr int kKv8MaxPos = INT32_MAX - 1024;     // positions stay within 32 bits
 constexpr float kKv8Least = 7.888609052210118e-31f;   // 2^-100: what is smaller throughout is stored as zeros
 
+// Pages of that many positions; the sum passes 32 bits.
+__host__ __device__ constexpr int64_t kv8_pages(int64_t positions) { return (positions + PAGE - 1) / PAGE; }
 // Record of page `page`, key head h.
 template <int D>
 __device__ __forceinline__ size_t kv8_record(int page, int heads, int h) {

@@ -321,7 +321,7 @@ inline int kv8_grid(int64_t rows, int64_t heads, int64_t pages, int limit) {
   return (int)(tiles < 1 ? 1 : (tiles < limit ? tiles : limit));
 }
 inline int kv8_wide_grid(int64_t rows, int64_t heads, int64_t max_entries, int num_sms) {
-  return kv8_grid(rows, heads, (max_entries + PAGE - 1) / PAGE, num_sms);
+  return kv8_grid(rows, heads, kv8_pages(max_entries), num_sms);
 }
 // The parts of cut segments in the workspace: records, (m, l), O / l.
 inline size_t kv8_parts_bytes(size_t grid, size_t cols, size_t dim) {

@@ -433,7 +433,7 @@ cudaError_t launch_score(const Kv8SelectArgs& a, dim3 grid, int per, int chunks,
   }
 }
 
-int32_t score_ld(int32_t max_entries) { return ((max_entries + PAGE - 1) / PAGE + 31) / 32 * 32; }
+int32_t score_ld(int32_t max_entries) { return (int32_t)((kv8_pages(max_entries) + 31) / 32 * 32); }
 
 }  // namespace
 
@@ -444,7 +444,7 @@ size_t kv8_select_ws_bytes(int32_t num_rows, int32_t max_entries, int32_t heads)
 cudaError_t launch_kv8_select(Kv8SelectArgs a, void* ws, cudaStream_t stream) {
   a.scores = static_cast<float*>(ws);
   a.ld = score_ld(a.rows.max_entries);
-  const int pages = (a.rows.max_entries + PAGE - 1) / PAGE;
+  const int pages = (int)kv8_pages(a.rows.max_entries);
   const int per = std::max(1, std::min(kScoreCols / a.G, a.rows.max_rows_per_req));
   // a CTA takes several chunks of pages where there are rows enough to fill the GPU (above)
   const int tiles = (a.rows.num_rows + per - 1) / per, chunks = (pages + kScoreThreads - 1) / kScoreThreads;

@@ -80,7 +80,7 @@ struct Smem {
   float factor[COLS];                            // of a column's logits (log2 units)
   float neg_m[COLS];                             // kTop minus the running maximum
   float neg_l[COLS];                             // minus the sums' own maximum, once scales are far apart
-  int far;                                       // a page's scale is, in this tile
+  int far, large;                                // a page's scale is, in this tile; a column's maximum is (kKv8Large)
   float red[4][COLS];                            // per warp: maxima of a tile, sums of p
   float corr[COLS];                              // correction of a column whose maximum moved; at the end 1 / l
   int out_row[COLS];                             // a column's row of the output
@@ -369,11 +369,22 @@ __device__ __noinline__ void own_sum(Smem<COLS, D>& sm, uint32_t tmem, uint32_t 
 #pragma unroll 1
   for (int c0 = 0; c0 < COLS; c0 += CH) {
     float z[CH];
-    s.logits(at, c0, sk, 0.0f, clo, true, sm.neg_l, z);
+    s.logits(at, c0, sk, 0.0f, clo, true, nullptr, z);
 #pragma unroll
-    for (int k = 0; k < CH; ++k) l[c0 + k] = fmaf(l[c0 + k], sm.corr[c0 + k], ex2(z[k]));
+    for (int k = 0; k < CH; ++k) l[c0 + k] = fmaf(l[c0 + k], sm.corr[c0 + k], ex2(z[k] + sm.neg_l[c0 + k]));
   }
   group_sync(1);                                 // red and corr are the next maximum's
+}
+// A tile's differences to its maxima where these are large (kKv8Large).
+template <int COLS, int D>
+__device__ __noinline__ void large_logits(Smem<COLS, D>& sm, uint32_t tmem, uint32_t at, float sk, float lsv, int clo, float* x) {
+  Logits<COLS, D> s{sm, tmem, (int)threadIdx.x, warp_id(), lane_id()};
+#pragma unroll 1
+  for (int c0 = 0; c0 < COLS; c0 += Logits<COLS, D>::CH) {
+    s.logits(at, c0, sk, lsv, clo, true, nullptr, x + c0);
+#pragma unroll 1
+    for (int k = 0; k < Logits<COLS, D>::CH; ++k) x[c0 + k] += sm.neg_m[c0 + k];
+  }
 }
 
 // O times neg_l, a factor by then.
@@ -488,6 +499,7 @@ struct Softmax : Logits<COLS, D> {
           // O of the tiles before is complete from here on
           ok = wait(&sm.p_free, (i & 1) ^ 1) && ok;
           if (lsv == INFINITY) sm.far = 1;
+          if (tid == 0) sm.large = 0;
           if (group_sync_or(2, !ok)) return false;
           tc_fence_after();
           if (sm.far) {
@@ -507,6 +519,7 @@ struct Softmax : Logits<COLS, D> {
             const float before = sm.neg_m[tid], now = fminf(before, kTop - tile_top());
             sm.corr[tid] = ex2(now - before);
             sm.neg_m[tid] = now;
+            if (fabsf(now) > kKv8Large && now < -kNoMax) sm.large = 1;
           }
           group_sync(1);
           if (w.t > w.t0) {
@@ -528,6 +541,12 @@ struct Softmax : Logits<COLS, D> {
           for (int c = 0; c < COLS; ++c) l[c] *= lref == -INFINITY ? 1.0f : sm.corr[c];
 #pragma unroll
           for (int c0 = 0; c0 < COLS; c0 += CH) logits(at, c0, sk, lsv, clo, masked, sm.neg_m, x + c0);
+          if (sm.large) {
+            float exact[COLS];
+            large_logits(sm, tmem, at, sk, lsv, clo, exact);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) x[c] = exact[c];
+          }
         } else {
           ok = wait(&sm.p_free, (i & 1) ^ 1) && ok;   // one that runs out ends the role at the next tile
         }

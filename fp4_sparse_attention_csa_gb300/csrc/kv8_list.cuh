@@ -222,6 +222,10 @@ struct Walk {
 // (two scales can be 96 apart, and the largest y is 2^6 at least), and one that fp32 no longer holds, below 2^-126, is
 // 2^-36 of that at most.
 constexpr float kKv8Near = 48.0f;
+// A logit's difference to the maximum is one fused step, off by half a step of the maximum: 2^-4 of a power of two at this
+// magnitude.  Beyond it that error would be the result, so the tile that moves the maximum rounds the logit first, as
+// the maximum was, and its largest y is what it should be.
+constexpr float kKv8Large = 1048576.0f;
 
 // ---- pages ---------------------------------------------------------------------------------
 // The pages of 16 tiles, one a lane: page number (INT_MAX: none) and pool page.

@@ -459,13 +459,38 @@ __device__ __noinline__ float own_sum(Smem<D>& sm, uint32_t scores, int x, int p
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         asm volatile("" : "+r"(u[k]));           // not before the wait
-        const float z = k0 + k < seen ? fmaf(__uint_as_float(u[k]), fs, base) : -INFINITY;
+        const float z = k0 + k < seen ? __fmul_rn(__uint_as_float(u[k]), fs) : -INFINITY;
         if (pass == 0) top = fmaxf(top, z);
-        else sum += ex2(z);
+        else sum += ex2(z + base);
       }
     }
   }
   return l + sum;
+}
+// y of the page's keys where maxima are large (kKv8Large), over the S that it came from; their sum.
+__device__ __noinline__ float large_probabilities(uint32_t scores, int seen, float fs, float lsv, float neg) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int k0 = 0; k0 < 64; k0 += 32) {
+    uint32_t u[32], y[16];
+    tmem_ld32(scores + k0, u);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      float z[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        asm volatile("" : "+r"(u[k + j]));       // not before the wait
+        // as `largest` rounds it; kTop minus the maximum is rounded, too, by up to 8
+        z[j] = k0 + k + j < seen ? ex2(fminf(fmaf(__uint_as_float(u[k + j]), fs, lsv) + neg, 15.0f)) : 0.0f;
+        sum += z[j];
+      }
+      y[k / 2] = f16x2_of(z[0], z[1]);
+    }
+    tmem_st16(scores + k0 / 2, y);
+    tmem_st_wait();
+  }
+  return sum;
 }
 template <int D>
 struct Softmax {
@@ -637,7 +662,15 @@ struct Softmax {
             }
           }
           sum = masked ? probabilities<true>(seen, fs, neg + lsv, y) : probabilities<false>(seen, fs, neg + lsv, y);
-          if (moves || !either(sum > kMost || !ok)) break;
+          if (moves) {
+            if (__any_sync(0xFFFFFFFFu, fabsf(neg) > kKv8Large && neg < -kNoMax)) {
+              sum = large_probabilities(scores, seen, fs, lsv, neg);
+              tmem_ld32(scores, y);
+              arrived(y);
+            }
+            break;
+          }
+          if (!either(sum > kMost || !ok)) break;
           moves = true;
         }
         l = fmaf(sum, isv, l);

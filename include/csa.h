@@ -611,10 +611,11 @@ CSA_API csa_status_t csa_kv8_append(const csa_kv8_t* cache, const csa_rope_t* ro
  * infinite or not a number gives NaN.
  *  Rounding: q enters as the sum of two E4M3 parts (exact down to 2^-9 of its largest
  * element, below that to 2^-17 of it), a probability times its value's scale as the sum
- * of three or as one fp16 number (to 2^-11 of itself or 2^-24 of the row's largest, however far
- * apart the scales of its pages lie);
- * keys and values are exact, sums and the softmax fp32.  Which is taken goes by the
- * shapes alone, and the results do not change from call to call.
+ * of three or as one fp16 number (to 2^-11 of itself or 2^-24 of the row's largest, however
+ * far apart the scales of its pages lie); keys and values are exact, sums and the softmax
+ * fp32.  Which is taken goes by the shapes alone, and the results do not change from call to
+ * call.  Logits may be as large as fp32 holds in units of ln 2; their differences are as
+ * exact as its steps at that size.
  *  q, out bf16 [R, n_heads, head_dim], 16-byte aligned; lse fp32 [R, n_heads] (nullable,
  * natural log).  out must not overlap any input.  ws: csa_workspace_size(
  * CSA_OP_KV8_ATTN, R, max_entries, n_heads) bytes, 256-byte aligned. */

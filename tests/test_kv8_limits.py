@@ -42,3 +42,52 @@ def test_rows_bounded_by_all_positions_there_are(rows, G):
     s.check([0] * rows, pos, q, out, lse, rows=[0, rows - 1])
     long, lse2 = s.attend([0] * rows, pos, q, most=1 << 20)
     assert np.array_equal(out, long) and np.array_equal(lse, lse2)
+
+
+@gpu
+@pytest.mark.parametrize("rows,G", [(1, 4), (2, 8), (4, 7), (3, 16), (20, 8), (9, 33)])
+@pytest.mark.parametrize("qs,ks,scale", [(300.0, 300.0, 1.0), (1e4, 1e4, 0.1), (1e6, 1e6, 1.0), (1e15, 1e15, 1.0), (1.0, 1.0, 1e25),
+                                         (1e4, 1e4, -0.1)])
+def test_logits_of_any_size(rows, G, qs, ks, scale):
+    """The largest logit 2^18 to 2^120, the next one far below it, or equal to it to the last bit: the output is the value
+    of the first, or the mean of the two, and the sum's logarithm that logit."""
+    d, n = 64, 700
+    rng = np.random.default_rng(rows + G)
+    k = np.sign(rng.standard_normal((n, 1, d))) * ks
+    v = bf16(rng.standard_normal((n, 1, d)))
+    for twins in (False, True):
+        q = np.empty((rows, G, d), np.float32)
+        best = rng.integers(0, n - rows, (rows, G))
+        other = (best + 64 * rng.integers(1, 9, (rows, G))) % (n - rows)
+        kk = k.copy()
+        if twins:
+            best[:], other[:] = 37, 437
+            kk[437] = kk[37]
+        kk = bf16(kk)
+        for r in range(rows):
+            for g in range(G):
+                q[r, g] = np.sign(kk[best[r, g], 0]) * (qs if scale > 0 else -qs)
+        q = bf16(q)
+        c = Cache(1, [n], 1, d, tokens=[(kk, v)])
+        s = Device(csa, c)
+        pos = list(range(n - rows, n))
+        out, lse = s.attend([0] * rows, pos, q, scale=scale)
+        assert s.flags == (0, 0)
+        pool = s.pool.cpu().numpy()
+        from kv8_ref import head_entries
+        key, val, _ = head_entries(pool, c.table[0], 0, d, np.arange(-(-n // 64)))
+        for r in range(rows):
+            x = (q[r].astype(np.float64) @ key[:pos[r] + 1].T) * scale
+            top = x.max(-1)
+            gap = top - np.where(np.arange(pos[r] + 1)[None] == best[r][:, None], -np.inf,
+                                 np.where(twins & (np.arange(pos[r] + 1) == 437), -np.inf, x)).max(-1)
+            assert (np.argmax(x, -1) == best[r]).all() and (gap > 2.0 ** -3 * np.abs(top)).all()   # keys' signs agree in some dims only
+            assert np.isfinite(lse[r]).all() and (np.abs(lse[r] - top) <= 1 + 2.0 ** -17 * np.abs(top)).all(), (r, lse[r], top)
+            want = (val[37] + val[437]) / 2 if twins else val[best[r]]
+            if twins and np.abs(top).max() < 2.0 ** 20:      # both in one fp32 difference
+                assert (np.abs(out[r] - want) <= 2.0 ** -6 * (1 + np.abs(want))).all()
+            elif twins:                                      # any mean of the two
+                lo, hi = np.minimum(val[37], val[437]), np.maximum(val[37], val[437])
+                assert ((out[r] >= lo - 2.0 ** -6 * (1 + np.abs(lo))) & (out[r] <= hi + 2.0 ** -6 * (1 + np.abs(hi)))).all()
+            else:
+                assert (np.abs(out[r] - want) <= 2.0 ** -7 * (1 + np.abs(want))).all()

@@ -252,7 +252,7 @@ struct Kv8AttnArgs {
   long long wait_budget;               // SM clocks a wait may take
   // set by the launcher: units of a step between segments, the workspace past the status word
   int32_t gap;
-  int4* rec;                           // [grid] a segment cut at the CTA's end: first row, rows | head << 8, first and last CTA
+  int4* rec;                           // [grid] a segment cut at the CTA's end: first row, rows | head << 16, first and last CTA
   float* part;                         // [2 * grid][cols][dim] O / l
   float* part_ml;                      // [2 * grid][2][cols] (m, l)
 };

@@ -100,12 +100,6 @@ __device__ __forceinline__ bool find_unit(const Kv8AppendArgs& a, int at, int* s
   return false;
 }
 
-// The largest magnitude of eight bf16, in both halves; NaN if there is one.
-__device__ __forceinline__ __nv_bfloat162 largest(uint4 v) {
-  auto two = [](uint32_t w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
-  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(two(v.x), two(v.y)), __hmax2_nan(two(v.z), two(v.w)));
-  return __hmax2_nan(m, __lowhigh2highlow(m));
-}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
@@ -181,11 +175,7 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) k_kv8_append(Kv8AppendA
         const int from = lane + (turn.other - i0) / 8;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          uint4 other;
-          other.x = __shfl_sync(0xFFFFFFFFu, raw[0][s].x, from);
-          other.y = __shfl_sync(0xFFFFFFFFu, raw[0][s].y, from);
-          other.z = __shfl_sync(0xFFFFFFFFu, raw[0][s].z, from);
-          other.w = __shfl_sync(0xFFFFFFFFu, raw[0][s].w, from);
+          const uint4 other = of_lane(raw[0][s], from);
           if (turns && ((is_new >> s) & 1u)) raw[0][s] = turn8(raw[0][s], other, a.rope, turn, p0 + s);
         }
       }
@@ -202,7 +192,7 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) k_kv8_append(Kv8AppendA
       // ---- amax of both sides; tokens that are not all numbers count as zeros from here on
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const float k = __low2float(largest(raw[0][t])), v = __low2float(largest(raw[1][t]));
+        const float k = __low2float(bf16x8_top(raw[0][t])), v = __low2float(bf16x8_top(raw[1][t]));
         const uint32_t row = ((1u << kPieces) - 1u) << (lane / kPieces * kPieces);
         const bool bad = !(k <= 3.4028234663852886e38f) || !(v <= 3.4028234663852886e38f);
         if (__ballot_sync(0xFFFFFFFFu, bad) & row) {

@@ -7,7 +7,7 @@
 // p = 2^(s - m), O^T += V^T P^T (M = dims), both products in E4M3 with fp32 sums on
 // operands as they lie in the pages: nothing is converted but Q and P.
 //   Q: a bf16 number has 8 bits and E4M3 holds 4, so a query scaled to [128, 256) is
-// hi + lo / 16 with E4M3 parts, exact but for elements below 2^-15 of the largest.  The
+// hi + lo / 16 with E4M3 parts, exact but for elements below 2^-13 of the largest.  The
 // parts are columns c and COLS + c of one product, S = S_hi + S_lo / 16.
 //   P: the page's value scale sv goes into the exponent, y = 2^(s + log2 sv - m) with m the
 // running maximum of s + log2 sv: what y is small against is then what its contribution to O
@@ -58,11 +58,11 @@ constexpr float kNoMax = -3e38f;                 // running maximum of a column 
 template <int COLS, int D>
 struct Shape {
   static constexpr int kStages = D == 64 ? 4 : 2;
-  static constexpr int kScoreBufs = COLS <= 32 ? 2 : 1;       // S of this many tiles in tensor memory
+  static constexpr int kScoreBufs = 2;                        // S of this many tiles in tensor memory
   static constexpr int kParts = (3 * COLS + 15) / 16 * 16;    // columns of P and O: hi, mid and lo, in whole sixteens
   static constexpr uint32_t kOut = kScoreBufs * 2 * COLS;     // tensor memory columns: S, then O's three parts
   static constexpr uint32_t kNeed = kOut + kParts;
-  static constexpr uint32_t kTmem = kNeed <= 64 ? 64 : (kNeed <= 128 ? 128 : (kNeed <= 256 ? 256 : 512));
+  static constexpr uint32_t kTmem = kNeed <= 64 ? 64 : (kNeed <= 128 ? 128 : 256);
   static constexpr int kValueSlot = 64 * D + 16;              // a page's values and its scales
   static constexpr int kStage = 128 * D + 2 * kValueSlot;
   static constexpr int kProbChunk = 128, kProbRows = 8 * kProbChunk;   // 16 keys, 8 columns of P
@@ -91,17 +91,6 @@ struct Smem {
   ShareScratch<kThreads> share;
 };
 
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// kind::f8f6f4, E4M3 operands, fp32 sums, both operands K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {
-  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
 
 // ---- pages ---------------------------------------------------------------------------------
 template <int COLS, int D>
@@ -225,7 +214,7 @@ struct Products {
     bool before = false, before_first = false, before_last = false, ok = true;   // the tile before: its P is not used yet
     for (bool more = w.first(a, RG, sh); more && w.settle(a, RG); ++i, ++w.t) {
       const bool first = w.t == w.t0, last = w.t + 1 == w.t_end;
-      if (before && (first || X::kScoreBufs == 1)) {
+      if (before && first) {
         if (!(ok = values(i - 1, before_first, before_last))) break;
         before = false;
       }
@@ -583,15 +572,7 @@ struct Softmax : Logits<COLS, D> {
         warp_arrive(&sm.p_full, lane);
       }
       // ---- the segment's output: sums over the keys' threads, then a dim a thread
-#pragma unroll
-      for (int c0 = 0; c0 < COLS; c0 += 32) {
-        constexpr int N = COLS < 32 ? COLS : 32;
-        float part[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k) part[k] = l[c0 + k];
-        const float t = warp_reduce_many<N, false>(part, lane);
-        sm.red[warp][c0 + lane / (32 / N)] = t;
-      }
+      sm.red[warp][lane / (32 / COLS)] = warp_reduce_many<COLS, false>(l, lane);
       ok = wait(&sm.o_full, outs++ & 1) && ok;
       if (group_sync_or(2, !ok)) return false;   // sums visible, too
       tc_fence_after();
@@ -643,7 +624,7 @@ struct Softmax : Logits<COLS, D> {
 
 // CTAs per SM: as many as shared memory holds with two tiles (four of 64 dims) under way in each.
 template <int COLS, int D>
-constexpr int kPerSm = COLS <= 16 ? 3 : (COLS <= 32 ? 2 : 1);
+constexpr int kPerSm = COLS <= 16 ? 3 : 2;
 
 template <int COLS, int D>
 __global__ void __launch_bounds__(kThreads, kPerSm<COLS, D>) k_kv8_attn(Kv8AttnArgs a, int RG) {

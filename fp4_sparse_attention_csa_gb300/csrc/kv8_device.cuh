@@ -80,6 +80,11 @@ __device__ __forceinline__ uint4 turn8(uint4 mine, uint4 other, const Kv8Rope& r
   }
   return f32_to_bf16x8(x);
 }
+// Another lane's piece.
+__device__ __forceinline__ uint4 of_lane(uint4 v, int from) {
+  return make_uint4(__shfl_sync(0xFFFFFFFFu, v.x, from), __shfl_sync(0xFFFFFFFFu, v.y, from),
+                    __shfl_sync(0xFFFFFFFFu, v.z, from), __shfl_sync(0xFFFFFFFFu, v.w, from));
+}
 // Dims i .. i + 7 (i a multiple of 8) of the head vector at vec, rotated at position pos.
 __device__ __forceinline__ uint4 rotated8(const uint16_t* vec, int i, const Kv8Rope& rope, int pos) {
   const uint4 raw = __ldg(reinterpret_cast<const uint4*>(vec + i));
@@ -100,17 +105,22 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The largest magnitude of a column of bf16, 8 each in LANES neighbouring lanes; NaN if there is one.
+// The largest magnitude of eight bf16, in both halves; NaN if there is one.
+__device__ __forceinline__ __nv_bfloat162 bf16x8_top(uint4 v) {
+  auto two = [](uint32_t w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(two(v.x), two(v.y)), __hmax2_nan(two(v.z), two(v.w)));
+  return __hmax2_nan(m, __lowhigh2highlow(m));
+}
+// That of a column, 8 each in LANES neighbouring lanes.
 template <int LANES>
 __device__ __forceinline__ float column_top(uint4 v) {
-  auto two = [](uint32_t w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
-  __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(two(v.x), two(v.y)), __hmax2_nan(two(v.z), two(v.w)));
+  __nv_bfloat162 m = bf16x8_top(v);
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) {
     const uint32_t w = __shfl_xor_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t*>(&m), o);
     m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&w));
   }
-  return __low2float(__hmax2_nan(m, __lowhigh2highlow(m)));
+  return __low2float(m);
 }
 
 }  // namespace csa

@@ -103,11 +103,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) k_kv8_score(Kv8SelectArgs a,
       if (c - tid / kPieces >= rows * G) break;
       if (rope.cos != nullptr) {                 // a pair's other half is another lane's of the same column
         const int from = lane + (turn.other - i0) / 8;
-        uint4 other;
-        other.x = __shfl_sync(0xFFFFFFFFu, raw[u].x, from);
-        other.y = __shfl_sync(0xFFFFFFFFu, raw[u].y, from);
-        other.z = __shfl_sync(0xFFFFFFFFu, raw[u].z, from);
-        other.w = __shfl_sync(0xFFFFFFFFu, raw[u].w, from);
+        const uint4 other = of_lane(raw[u], from);
         if (turns && c < rows * G && s_end[c / G] > 0) raw[u] = turn8(raw[u], other, rope, turn, s_pos[c / G]);
       }
       float top = column_top<kPieces>(raw[u]);

@@ -93,13 +93,6 @@ struct Smem {
   ShareScratch<kThreads> share;
 };
 
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 __device__ __forceinline__ uint32_t f16x2_of(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -269,7 +262,7 @@ struct Products {
   __device__ __forceinline__ On formed(int x) { return On{&sm.p_full[x], (used >> x) & 1}; }
   // S of half x and tile i, with the queries of half qx; the last half to use the keys gives them back
   __device__ __forceinline__ void scores(int x, int qx, uint32_t i, bool last_half) {
-    constexpr uint32_t idesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);     // E4M3, M = N = 128
+    constexpr uint32_t idesc = idesc_e4m3(128, 128);
     tc_fence_after();
     const uint64_t k = smem_desc(smem_u32(sm.k[0]), 128, 8 * D, kSwizzleNone) + (i % X::kKeyStages) * (8 * D);
     const uint64_t q = smem_desc(smem_u32(sm.q[0][0]), 128, 8 * D, kSwizzleNone) + qx * (kHalf * D / 8);

@@ -522,10 +522,13 @@ CSA_API csa_status_t csa_pages_compact(const csa_cache_t* cache, const csa_pages
 
 /* ---- 8-bit cache of keys and values with grouped heads ----------------------------
  * For the layers of a model that keep a key and a value per token and key head
- * next to those that read the shared latent: the same pages of 64 positions, page
- * tables and query rows, in E4M3 with a scale per page, key head and side.  The
- * calls follow the ones above: append, rank pages (csa_kv8_select), attend to the
- * ranked pages (csa_kv8_block_attn) or to everything (csa_kv8_attn).
+ * next to those that read the shared latent, in E4M3 with a scale per page, key head
+ * and side.  The calls follow the ones above: append, rank pages (csa_kv8_select), attend
+ * to the ranked pages (csa_kv8_block_attn) or to everything (csa_kv8_attn).
+ *  Pages are 64 positions, so where a latent entry is one token (pool_ratio 1) one page
+ * table and one csa_rows_t serve both caches.  Where it pools two, a latent page is 128
+ * positions: this cache has a page table of its own and a csa_rows_t whose max_entries
+ * bounds position + 1; the arrays of rows are shared.
  *
  * FORMAT.  Page p of key head h is a record of CSA_KV8_RECORD_BYTES(d) bytes at
  * pool + (p * n_kv_heads + h) * CSA_KV8_RECORD_BYTES(d), d = head_dim:

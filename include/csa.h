@@ -550,12 +550,17 @@ CSA_API csa_status_t csa_pages_compact(const csa_cache_t* cache, const csa_pages
  *   tail: the keys (rotated) and values of each request's last 128 positions in
  * bf16; position p is in slot p % 128.  An unfinished page is quantised anew from
  * it at each append, so a page's bytes depend only on its tokens, however they were
- * split into calls, and the last 64 positions can be appended again with other
- * tokens (drafts that were rejected).  A page is written whole, so one shared by two
- * requests needs no copy before one of them continues: it needs a page of its own
- * and the parent's tail.  The page calls above serve a page table that both kinds of
- * cache use, but move the latent's pages alone: csa_pages_compact renumbers pages, so
- * a table with a cache of this kind behind it is not for it. */
+ * split into calls, and tokens can be appended again with others in their place (drafts
+ * that were rejected).  An append from position p needs the positions from p's page's
+ * start up to p in the tail: with N - 1 the highest position that was ever written,
+ * rejected ones among them, p may be N - 64 or more.  Nothing detects an append from
+ * further back.
+ *  A page is written whole, so one shared by two requests needs no copy before one of
+ * them continues: it needs a page of its own (csa_pages_reserve gives it one) and the
+ * parent's tail, which the caller copies and which serves a child that continues from at
+ * most 64 positions before the parent's end.  The page calls move the latent's pages
+ * alone: csa_pages_compact renumbers pages, so a table with a cache of this kind behind it
+ * is not for it. */
 #define CSA_KV8_RECORD_BYTES(d) (128 * (d) + 128)
 #define CSA_KV8_TAIL          128   /* positions of the tail                     */
 #define CSA_KV8_MAX_HEADS     1024  /* query heads; n_kv_heads 1..256, and query

@@ -91,3 +91,27 @@ def test_logits_of_any_size(rows, G, qs, ks, scale):
                 assert ((out[r] >= lo - 2.0 ** -6 * (1 + np.abs(lo))) & (out[r] <= hi + 2.0 ** -6 * (1 + np.abs(hi)))).all()
             else:
                 assert (np.abs(out[r] - want) <= 2.0 ** -7 * (1 + np.abs(want))).all()
+
+
+@gpu
+@pytest.mark.parametrize("seed", range(4))
+def test_drafts_rejected_time_and_again(seed):
+    """Appends from anywhere down to 64 below the highest position that was ever written: in the end pages, summaries
+    and tail are those of the tokens that stayed."""
+    n = 700
+    c = Cache(30 + seed, [n], 2, 64)
+    s = Device(csa, c, filled=False)
+    rng = np.random.default_rng(seed)
+    kept = most = calls = 0                                # tokens that stay; one past the highest position written
+    while kept < n:
+        lo = int(rng.integers(max(0, most - 64), kept + 1)) if calls % 2 else kept
+        new = int(min(rng.integers(1, 65), n - lo))
+        stay = new if calls % 3 == 0 else int(rng.integers(0, new + 1))
+        s.append([lo], [new], *(np.concatenate([x[lo:lo + stay], bf16(rng.standard_normal((new - stay, 2, 64)))])
+                                for x in c.tokens[0]))
+        kept, most, calls = lo + stay, max(most, lo + new), calls + 1
+    assert s.status() == (0, 0) and calls > 20
+    pool, codes, scale, tail = c.fill()
+    assert np.array_equal(s.pool.cpu().numpy(), pool)
+    assert np.array_equal(s.codes.cpu().numpy(), codes) and np.array_equal(s.scale.cpu().numpy(), scale)
+    assert np.array_equal(s.tail.float().cpu().numpy(), tail)

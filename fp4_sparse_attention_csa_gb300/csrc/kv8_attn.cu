@@ -672,16 +672,65 @@ __global__ void __launch_bounds__(kThreads, kPerSm<COLS, D>) k_kv8_attn(Kv8AttnA
 
 // ---- cut segments -----------------------------------------------------------------------------
 // A row of CTAs a cut, W warps a column; a warp sums its parts' O / l by their weights l 2^m, in the
-// parts' order.  Weights count in 2^40: l grows with a part's keys, and O / l can be as large as a value.  Of their
-// sum's leading term, 2^-82 at least (kKv8Near), what fp32 drops is less than 2^-44.
-// Bound by latency: statistics and a warp's first 8 parts are asked for at once, 3.4 us for the 33 parts
-// of one token after 4096.
-constexpr int kMergeThreads = 512;
+// parts' order.  A part's weight can be 2^-228 of another's and still bring most of the output, by its values (their
+// scales span as much); where weights are that far apart they are applied as two factors.  Taken with l in [1, 2),
+// the largest weight is 2^-11 of that: with fewer than 2^10 parts no sum leaves fp32's range at either end.
+// Bound by latency: statistics and a warp's first 8 parts are asked for at once, some 3 us for the 33 parts
+// of one token after 4096.  CTAs of 512 threads, with 64 registers each, took 0.5 us more, and 4 for 64 rows' lists.
+constexpr int kMergeThreads = 256, kMergePerSm = 3;
+constexpr float kPartUnit = 1.0f / 2048.0f, kDeep = -64.0f;
+// A part's slot: 2 c0 + 1 of the first, then 2 (c0 + 1), 2 (c0 + 2), ...
+__device__ __forceinline__ size_t part_slot(int first, int q) { return (size_t)(q == 0 ? 2 * first + 1 : 2 * (first + q)); }
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads, 2) k_kv8_merge(Kv8AttnArgs a, int cols_max) {
+__device__ __forceinline__ void write_column(uint16_t* out, float* lse, const float (&acc)[D / 32], float M, float L) {
+  constexpr int N = D / 32;
+  const int lane = lane_id();
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  uint32_t o[N / 2];
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    const __nv_bfloat162 z = __floats2bfloat162_rn(inv == 0.0f ? 0.0f : acc[j] * inv, inv == 0.0f ? 0.0f : acc[j + 1] * inv);
+    o[j / 2] = *reinterpret_cast<const uint32_t*>(&z);
+  }
+  uint16_t* dst = out + N * lane;
+  if constexpr (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = o[0];
+  if (lse && lane == 0) *lse = L == 0.0f ? -INFINITY : (M + log2f(L * (1.0f / kPartUnit))) * kLn2;
+}
+// (m, l) of a part, l as a number in [1, 2) whose power of two m takes up; 0, infinities and NaN as they are, or twice over.
+__device__ __forceinline__ float2 part_stats(const float* part_ml, int cols_max, int c, int first, int q) {
+  const float* ml = part_ml + part_slot(first, q) * 2 * cols_max + c;
+  const float m = __ldcg(ml), l = __ldcg(ml + cols_max);
+  const int e = l > 0.0f ? min(126, (int)(__float_as_uint(l) >> 23) - 127) : 0;
+  return make_float2(m + (float)e, l * pow2(-e));
+}
+// A column whose parts' weights are far apart, by one warp.  Seldom called, and kept out of the way.
+template <int D>
+__device__ __noinline__ void deep_column(const float* part, const float* part_ml, int cols_max, int c, int first, int n,
+                                         uint16_t* out, float* lse) {
+  constexpr int N = D / 32;
+  float M = kNoMax, L = 0.0f, acc[N];
+#pragma unroll 1
+  for (int q = 0; q < n; ++q) M = fmaxf(M, part_stats(part_ml, cols_max, c, first, q).x);
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+#pragma unroll 1
+  for (int q = 0; q < n; ++q) {
+    const float2 ml = part_stats(part_ml, cols_max, c, first, q);
+    const float d = ml.x - M, f = ex2(d < kDeep ? 0.5f * d : d), g = d < kDeep ? f : 1.0f;
+    const float w = f * ml.y * kPartUnit;
+    L = fmaf(w, g, L);
+    const float* v = part + (part_slot(first, q) * cols_max + c) * D + N * lane_id();
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = fmaf(w, __ldcg(v + j) * g, acc[j]);
+  }
+  write_column<D>(out, lse, acc, M, L);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads, kMergePerSm) k_kv8_merge(Kv8AttnArgs a, int cols_max) {
   constexpr int N = D / 32, kWarps = kMergeThreads / 32;
-  constexpr float kUnit = 9.094947017729282e-13f;            // 2^-40
   __shared__ float s_o[kWarps][D];
   const int warp = warp_id(), lane = lane_id();
   pdl_wait();
@@ -690,11 +739,11 @@ __global__ void __launch_bounds__(kMergeThreads, 2) k_kv8_merge(Kv8AttnArgs a, i
   const int g = rec.y & 0xFFFF, h = rec.y >> 16, G = a.G, cols = g * G, n = rec.w - rec.z + 1;
   int W = 1;
   while (2 * W * cols <= kWarps) W *= 2;
-  // a part's slot: 2 c0 + 1 of the first, then 2 (c0 + 1), 2 (c0 + 2), ...
-  auto slot = [&](int q) { return (size_t)(q == 0 ? 2 * rec.z + 1 : 2 * (rec.z + q)); };
+  auto slot = [&](int q) { return part_slot(rec.z, q); };
   for (int c0 = blockIdx.y * (kWarps / W); c0 < cols; c0 += gridDim.y * (kWarps / W)) {
     const int c = c0 + warp / W, sub = warp % W;
     float M = kNoMax, L = 0.0f, acc[N];
+    float least = INFINITY;                      // of the lane's parts' m
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.0f;
     if (c < cols) {
@@ -704,9 +753,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) k_kv8_merge(Kv8AttnArgs a, i
         const int q = base + lane, end = min(32, n - base);
         float m = kNoMax, l = 0.0f;
         if (q < n) {
-          const float* ml = a.part_ml + slot(q) * 2 * cols_max + c;
-          m = __ldcg(ml);
-          l = __ldcg(ml + cols_max);
+          const float2 ml = part_stats(a.part_ml, cols_max, c, rec.z, q);
+          m = ml.x;
+          l = ml.y;
         }
         float wgt = 0.0f;
 #pragma unroll 1
@@ -720,9 +769,11 @@ __global__ void __launch_bounds__(kMergeThreads, 2) k_kv8_merge(Kv8AttnArgs a, i
             else *reinterpret_cast<float2*>(v[i]) = __ldcg(reinterpret_cast<const float2*>(src));
           }
           if (k0 == sub) {
-            const float now = fmaxf(M, warp_top(m)), corr = ex2(M - now);
+            const float now = fmaxf(M, warp_top(m));
+            const float corr = ex2(M - now);
+            least = fminf(least, l == 0.0f ? INFINITY : m);
             M = now;
-            wgt = ex2(m - now) * l * kUnit;
+            wgt = ex2(m - now) * l * kPartUnit;
             L = fmaf(L, corr, wgt);
 #pragma unroll
             for (int j = 0; j < N; ++j) acc[j] *= corr;
@@ -752,17 +803,10 @@ __global__ void __launch_bounds__(kMergeThreads, 2) k_kv8_merge(Kv8AttnArgs a, i
     if (sub == 0 && c < cols) {
       const int i = c / G;
       const size_t row = (size_t)(rec.x + i) * a.heads * G + h * G + (c - i * G);
-      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-      uint32_t o[N / 2];
-#pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        const __nv_bfloat162 z = __floats2bfloat162_rn(inv == 0.0f ? 0.0f : acc[j] * inv, inv == 0.0f ? 0.0f : acc[j + 1] * inv);
-        o[j / 2] = *reinterpret_cast<const uint32_t*>(&z);
-      }
-      uint16_t* dst = a.out + row * D + N * lane;
-      if constexpr (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
-      else *reinterpret_cast<uint32_t*>(dst) = o[0];
-      if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L * (1.0f / kUnit))) * kLn2;
+      uint16_t* out = a.out + row * D;
+      float* lse = a.lse ? a.lse + row : nullptr;
+      if (__any_sync(0xFFFFFFFFu, least - M < kDeep)) deep_column<D>(a.part, a.part_ml, cols_max, c, rec.z, n, out, lse);
+      else write_column<D>(out, lse, acc, M, L);
     }
   }
 }
@@ -810,8 +854,8 @@ cudaError_t launch_dim(const Kv8AttnArgs& a, uint8_t* ws, int num_sms, cudaStrea
 
 cudaError_t launch_kv8_merge(const Kv8AttnArgs& a, int cols, int grid, cudaStream_t stream) {
   if (a.dim == 64)
-    return launch_kernel(Order::kChained, k_kv8_merge<64>, dim3(grid - 1, (cols + 15) / 16), dim3(kMergeThreads), 0, stream, a, cols);
-  return launch_kernel(Order::kChained, k_kv8_merge<128>, dim3(grid - 1, (cols + 15) / 16), dim3(kMergeThreads), 0, stream, a, cols);
+    return launch_kernel(Order::kChained, k_kv8_merge<64>, dim3(grid - 1, std::min((cols + 7) / 8, 16)), dim3(kMergeThreads), 0, stream, a, cols);
+  return launch_kernel(Order::kChained, k_kv8_merge<128>, dim3(grid - 1, std::min((cols + 7) / 8, 16)), dim3(kMergeThreads), 0, stream, a, cols);
 }
 
 // For any split of the heads into groups and any number of pages up to max_entries'.

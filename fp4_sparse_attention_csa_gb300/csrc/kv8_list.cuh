@@ -231,10 +231,10 @@ struct Walk {
 
 // ---- sums ----------------------------------------------------------------------------------
 // Value scales of a segment are near one another up to this many powers of two beside its first tile's.  There the
-// probabilities that the products take, y <= 2^15, serve the sum as well: the key that makes most of it has y >= 2^-90
-// (two scales can be 96 apart, and the largest y is 2^6 at least), and one that fp32 no longer holds, below 2^-126, is
-// 2^-36 of that at most.
-constexpr float kKv8Near = 48.0f;
+// probabilities that the products take, y <= 2^15, serve the sum as well: the key that makes most of it has y >= 2^-26
+// (two scales can be 32 apart, and the largest y is 2^6 at least), one that fp32 no longer holds, below 2^-126, is
+// nothing beside it, and the units' power of two, which the sum's maximum takes up, costs that a bit or two.
+constexpr float kKv8Near = 16.0f;
 // A logit's difference to the maximum is one fused step, off by half a step of the maximum: 2^-4 of a power of two at this
 // magnitude.  Beyond it that error would be the result, so the tile that moves the maximum rounds the logit first, as
 // the maximum was, and its largest y is what it should be.

@@ -195,3 +195,21 @@ def test_listed_pages_of_no_values_and_far_scales(rows, G):
     scales = [0, 1e-5, 1e10, 0, 1e-25, 1, 1]
     run(3, 1200, rows, G, 64, scales, [bits(c, 64) for c in (5, 0, -60, 100, 80)], lists=[[[0, 3, 7, 8, 10, 11, 14]]])
     run(4, 1200, rows, G, 64, scales, [0.0], lists=[[[1, 2, 4, 18]]])
+
+
+@gpu
+@pytest.mark.parametrize("rows,G", [(1, 8), (1, 16), (1, 32), (20, 8)])
+@pytest.mark.parametrize("scale", [1e-25, 1e-29])
+def test_small_values_in_cut_rows(rows, G, scale):
+    long_row(12000, 1, 128, [scale], [0.0], rows, G)
+
+
+@gpu
+@pytest.mark.parametrize("rows,G", [(1, 4), (1, 16), (1, 32), (9, 7)])
+def test_parts_of_small_weight_and_large_values(rows, G):
+    """Parts whose sums are up to 2^-220 of another's and whose values make up for it."""
+    for seed in range(24):
+        rng = np.random.default_rng(seed)
+        n = int(rng.integers(130, 1000))
+        pages = -(-n // PAGE)
+        run(seed, n, min(rows, n), G, 64, 10.0 ** rng.uniform(-28, 34, pages), bits(rng.uniform(-150, 150, pages), 64))

@@ -213,3 +213,21 @@ def test_parts_of_small_weight_and_large_values(rows, G):
         n = int(rng.integers(130, 1000))
         pages = -(-n // PAGE)
         run(seed, n, min(rows, n), G, 64, 10.0 ** rng.uniform(-28, 34, pages), bits(rng.uniform(-150, 150, pages), 64))
+
+
+@gpu
+@pytest.mark.parametrize("rows,G", [(1, 8), (6, 16), (40, 8)])
+@pytest.mark.parametrize("budget", [200, 3000, 20000])
+def test_waits_that_run_out_among_far_scales(rows, G, budget):
+    """A short limit for each wait: the call returns whatever it got to, and the next one is right."""
+    scales = [1, 1, 0, 1e12, 1, 1e-9, 1, 1]
+    s, q, out, lse = long_row(5000, 2, 128, scales, bits(np.array([0, 3, 9, -40, 0, 25]), 128), rows, G)
+    pos = list(range(5000 - rows, 5000))
+    csa.csa_set_wait_budget(budget)                        # SM clocks; the shortest is less than any copy takes
+    try:
+        s.attend([0] * rows, pos, q)
+        assert s.flags in ((0, 0), (6, csa.FLAG_TIMEOUT)) and (budget > 200 or s.flags[0] == 6)
+    finally:
+        csa.csa_set_wait_budget(0)
+    again, lse2 = s.attend([0] * rows, pos, q)
+    assert s.flags == (0, 0) and np.array_equal(out, again) and np.array_equal(lse, lse2)

@@ -14,7 +14,7 @@
 // in 16-byte pieces.
 //
 // What bounds it.  A small call: one dependent chain (offsets, page, tokens, amax, codes) in
-// each CTA, 4.7 us for a token of 8 heads of 128.  128 requests' single tokens take 13.9 us, 2.5
+// each CTA, 4.7 us for a token of 8 heads of 128.  128 requests' single tokens take 13.8 us, 2.5
 // TB/s of the bytes that they must move: the chain again, in 1024 CTAs of which 608 run at once (a
 // warp for the search alone took 19.9 us).  A prompt's 4 x 4001 tokens with half of each key rotated
 // take 39 us, 2.7 TB/s: a warp issues 1360 instructions a page for rotation, amax, sums and codes, in

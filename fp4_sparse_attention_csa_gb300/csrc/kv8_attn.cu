@@ -30,15 +30,15 @@
 // per SM overlap one another's chains, so inside a CTA only the copies run ahead.
 //
 // What bounds it.  With few columns HBM: 64 rows of 64 heads over 8 key heads of 128 at 4k to 64k
-// tokens take 436 us for the 2.91 GB that they have to read, 6.68 TB/s of 6.68 measured for a copy.
-// Lists of 16 pages for each of 2048 rows read 4.3 GB from L2 in 482 us, 9.0 TB/s: the chain of a
+// tokens take 435 us for the 2.91 GB that they have to read, 6.68 TB/s of 6.68 measured for a copy.
+// Lists of 16 pages for each of 2048 rows read 4.3 GB from L2 in 486 us, 8.9 TB/s: the chain of a
 // tile (2200 clocks: S, probabilities, their product) and of a step between segments (another 5600:
 // output, queries, first maximum), each overlapped by the two other CTAs of the SM; queries asked for
 // ahead of the output before them left the time as it was.  One token after
-// 4096 takes 11.5 us, one step after another: 6.3 to the last part's end, 1.1 until the join begins,
-// 3.4 to its end.  From 16 columns on the softmax's instructions count, each column's three parts above
-// all: 32 requests at 4k to 6k tokens, 4 key heads of 64, take 28 us with 7 columns a group, 36 with
-// 14 and 56 with 28.
+// 4096 takes 11.3 us, one step after another: the parts more than half of it, some 1 until the join
+// begins, the rest in it.  From 16 columns on the softmax's instructions count, each column's three parts above
+// all: 32 requests at 4k to 6k tokens, 4 key heads of 64, take 27 us with 7 columns a group, 35 with
+// 14 and 57 with 28.  Segments whose value scales are far apart read each tile's logits three times.
 #include <algorithm>
 
 #include "kv8_list.cuh"

@@ -611,9 +611,10 @@ CSA_API csa_status_t csa_kv8_append(const csa_kv8_t* cache, const csa_rope_t* ro
  * to the row's own; n_heads query heads, head i reads key head i / (n_heads /
  * n_kv_heads).  For single tokens, verify rows and prompt chunks (rows of a request at
  * consecutive positions share its keys); append the rows' tokens first.
- *  rows.max_entries: host bound on position + 1; rope nullable: q is rotated with each
- * row's position and rounded to bf16 (so the result is that of a call with q rotated
- * before it).  A row whose request or position is out of range raises
+ *  rows.max_entries: host bound on position + 1; rows.max_rows_per_req: the call's kernel
+ * goes by it, so prompt chunks and single rows are faster in a call each; rope nullable:
+ * q is rotated with each row's position and rounded to bf16 (so the result is that of a
+ * call with q rotated before it).  A row whose request or position is out of range raises
  * CSA_FLAG_ROW_INVALID and gets a zero output and lse -inf; a page whose id is out of
  * range is left out and raises CSA_FLAG_PAGE_OOB.  A query with an element that is
  * infinite or not a number gives NaN.
@@ -654,7 +655,8 @@ CSA_API csa_status_t csa_kv8_select(const csa_kv8_t* cache, const csa_rows_t* ro
  * n_blocks], strictly ascending, ended by -1 or n_blocks entries (csa_kv8_select's
  * output, or a caller's own).  Positions past the row's own are not seen.  An entry
  * past the row's page, or not above all that count before it, is left out and raises
- * CSA_FLAG_TOPK_OOB; a row that lists nothing gets a zero output and lse -inf. */
+ * CSA_FLAG_TOPK_OOB; a row that lists nothing gets a zero output and lse -inf.  Rows share
+ * nothing here: for the rows of a prompt csa_kv8_attn over all pages is the faster call. */
 CSA_API csa_status_t csa_kv8_block_attn(const csa_kv8_t* cache, const csa_rows_t* rows, const int32_t* blocks,
                                         int32_t n_blocks, int32_t n_heads, const void* q, const csa_rope_t* rope,
                                         float softmax_scale, void* out, float* lse, void* ws, size_t ws_bytes,

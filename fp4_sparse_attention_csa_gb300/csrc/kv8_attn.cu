@@ -342,27 +342,47 @@ struct Logits {
   }
 };
 
-// l with this tile's keys, where sums have a maximum of their own.  units: of l, which so far counts from neg_m; -inf: it had
-// such a maximum before.  All threads of the four warps.  Seldom called, and kept out of the loop that calls it.
+// A tile where sums have a maximum of their own: l, O's corrections and the logits from its maxima.  l counts from neg_l,
+// minus the largest s, and O from neg_l + neg_m: a difference of two large numbers would say nothing of value scales.
+// units: of l in the first such tile, where it and O count from neg_m; -inf in later ones.  All threads of the four warps.
+// Seldom called, and kept out of the loop that calls it.
 template <int COLS, int D>
-__device__ __noinline__ void own_sum(Smem<COLS, D>& sm, uint32_t tmem, uint32_t at, float sk, int clo, float units, float* l) {
+__device__ __noinline__ void far_tile(Smem<COLS, D>& sm, uint32_t tmem, uint32_t at, float sk, float lsv, int clo, float units,
+                                      float* l, float* x) {
   Logits<COLS, D> s{sm, tmem, (int)threadIdx.x, warp_id(), lane_id()};
   constexpr int CH = Logits<COLS, D>::CH;
+  float rel = 0.0f, shift = 0.0f;
   s.tile_tops(at, sk, 0.0f, clo, true);
   if (s.tid < COLS) {
-    const float before = units == -INFINITY ? sm.neg_l[s.tid] : sm.neg_m[s.tid] + units, now = fminf(before, -s.tile_top());
-    sm.corr[s.tid] = ex2(now - before);
+    const float n = sm.neg_m[s.tid], before = units == -INFINITY ? sm.neg_l[s.tid] : n + units;
+    const float now = fminf(before, -s.tile_top());
+    rel = units == -INFINITY || !(n < -kNoMax) ? n : -units;          // that of a column that has seen nothing stays so
+    shift = now - before;
+    sm.corr[s.tid] = ex2(shift);
     sm.neg_l[s.tid] = now;
   }
   group_sync(1);
 #pragma unroll 1
   for (int c0 = 0; c0 < COLS; c0 += CH) {
-    float z[CH];
-    s.logits(at, c0, sk, 0.0f, clo, true, nullptr, z);
-#pragma unroll
-    for (int k = 0; k < CH; ++k) l[c0 + k] = fmaf(l[c0 + k], sm.corr[c0 + k], ex2(z[k] + sm.neg_l[c0 + k]));
+    s.logits(at, c0, sk, 0.0f, clo, true, nullptr, x + c0);
+#pragma unroll 1
+    for (int c = c0; c < c0 + CH; ++c) {
+      x[c] += sm.neg_l[c];
+      l[c] = fmaf(l[c], sm.corr[c], ex2(x[c]));
+      x[c] += lsv;
+      const float t = warp_top(x[c]);
+      if (s.lane == 0) sm.red[s.warp][c] = t;
+    }
   }
-  group_sync(1);                                 // red and corr are the next maximum's
+  group_sync(1);
+  if (s.tid < COLS) {
+    const float next = fminf(rel < -kNoMax ? rel - shift : rel, kTop - s.tile_top());
+    sm.corr[s.tid] = ex2(shift + (next - rel));
+    sm.neg_m[s.tid] = next;
+  }
+  group_sync(1);
+#pragma unroll 1
+  for (int c = 0; c < COLS; ++c) x[c] += sm.neg_m[c];
 }
 // A tile's differences to its maxima where these are large (kKv8Large).
 template <int COLS, int D>
@@ -491,26 +511,29 @@ struct Softmax : Logits<COLS, D> {
           if (tid == 0) sm.large = 0;
           if (group_sync_or(2, !ok)) return false;
           tc_fence_after();
-          if (sm.far) {
+          const bool far = sm.far;
+          float exact[COLS];
+          if (far) {
             float keep[COLS];
 #pragma unroll
             for (int c = 0; c < COLS; ++c) keep[c] = l[c];
-            own_sum(sm, tmem, at, sk, clo, w.t > w.t0 ? lref : 0.0f, keep);
+            const float own = base != INT_MAX ? log2f(scales(page).y) : 0.0f;
+            far_tile(sm, tmem, at, sk, own, clo, w.t > w.t0 ? lref : 0.0f, keep, exact);
 #pragma unroll
             for (int c = 0; c < COLS; ++c) l[c] = keep[c];
             lref = -INFINITY;
             isv = 0.0f;
-            lsv = log2f(scales(page).y);         // of a page that is not there anything
+            if (tid == 0) sm.far = 0;
+          } else {
+            tile_tops(at, sk, lsv, clo, masked);
+            if (tid < COLS) {
+              const float before = sm.neg_m[tid], now = fminf(before, kTop - tile_top());
+              sm.corr[tid] = ex2(now - before);
+              sm.neg_m[tid] = now;
+              if (fabsf(now) > kKv8Large && now < -kNoMax) sm.large = 1;
+            }
+            group_sync(1);
           }
-          tile_tops(at, sk, lsv, clo, masked);
-          if (tid == 0) sm.far = 0;
-          if (tid < COLS) {
-            const float before = sm.neg_m[tid], now = fminf(before, kTop - tile_top());
-            sm.corr[tid] = ex2(now - before);
-            sm.neg_m[tid] = now;
-            if (fabsf(now) > kKv8Large && now < -kNoMax) sm.large = 1;
-          }
-          group_sync(1);
           if (w.t > w.t0) {
 #pragma unroll 1
             for (int c0 = 0; c0 < X::kParts; c0 += 16) {
@@ -527,12 +550,13 @@ struct Softmax : Logits<COLS, D> {
             tmem_st_wait();
           }
 #pragma unroll
-          for (int c = 0; c < COLS; ++c) l[c] *= lref == -INFINITY ? 1.0f : sm.corr[c];
+          for (int c = 0; c < COLS; ++c) l[c] *= far ? 1.0f : sm.corr[c];
+          if (!far) {
 #pragma unroll
-          for (int c0 = 0; c0 < COLS; c0 += CH) logits(at, c0, sk, lsv, clo, masked, sm.neg_m, x + c0);
-          if (sm.large) {
-            float exact[COLS];
-            large_logits(sm, tmem, at, sk, lsv, clo, exact);
+            for (int c0 = 0; c0 < COLS; c0 += CH) logits(at, c0, sk, lsv, clo, masked, sm.neg_m, x + c0);
+            if (sm.large) large_logits(sm, tmem, at, sk, lsv, clo, exact);
+          }
+          if (far || sm.large) {
 #pragma unroll
             for (int c = 0; c < COLS; ++c) x[c] = exact[c];
           }
@@ -582,7 +606,7 @@ struct Softmax : Logits<COLS, D> {
         // O counts in 2^-neg_m, l in 2^m
         const bool far = lref == -INFINITY;
         const float m = far ? -sm.neg_l[tid] : -(sm.neg_m[tid] + lref);
-        const float up = far ? ex2(-0.5f * (m + sm.neg_m[tid])) : pow2((int)lref);   // by halves: all of it may pass fp32's range
+        const float up = far ? ex2(-0.5f * sm.neg_m[tid]) : pow2((int)lref);   // by halves: all of it may pass fp32's range
         if (far) sm.neg_l[tid] = up;
         sm.corr[tid] = sum == 0.0f ? 0.0f : up / sum;
         if (whole) {

@@ -86,7 +86,8 @@ struct Smem {
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain;
   float2 joined[2][kHalf];                       // half b's -maximum and its pages' sums of a shared tile of columns
   float pair[2][2][kHalf];                       // [half][page]: what the two threads of a column tell one another
-  float own_top[2][2][kHalf], own_neg[2][2][kHalf];   // sums with a maximum of their own: a page's, minus the column's (NaN: not so)
+  // sums with a maximum of their own: a page's, minus the column's (NaN: not so), and what O counts from beside that
+  float own_top[2][2][kHalf], own_neg[2][2][kHalf], own_rel[2][2][kHalf];
   uint64_t b_full, b_free;                       // these and half b's O: complete, read
   uint32_t tmem_base;
   volatile int abort;                            // a wait ran out: every role leaves
@@ -426,39 +427,82 @@ __device__ __forceinline__ void convert_queries(const Kv8AttnArgs& a, Smem<D>& s
 }
 
 // ---- softmax ---------------------------------------------------------------------------------------
-// l of a column's page with this tile's keys, where sums have a maximum of their own.  own_neg is minus that, in units
-// of 2^lref as the probabilities' is, `neg` so far.  The two warps that share the columns meet once.  Seldom called, and
-// kept out of the loop that calls it.
+// A tile of a column's page where sums have a maximum of their own: l, and the factor of O.  y goes over the S that it came
+// from.  l counts from own_neg, minus the largest s, and O from own_neg + own_rel: a difference of two large numbers would
+// say nothing of value scales.  In the first such tile l counts from neg + lref and O from neg.  The two warps that share
+// the columns meet twice.  Seldom called, and kept out of the loop that calls it.
 template <int D>
-__device__ __noinline__ float own_sum(Smem<D>& sm, uint32_t scores, int x, int p, int c, int seen, float fs, float neg, float lref, float l) {
-  float top = -INFINITY, sum = 0.0f, base = 0.0f;
+__device__ __noinline__ float2 far_tile(Smem<D>& sm, uint32_t scores, int x, int p, int c, int seen, float fs, float lsv, float neg,
+                                        float lref, float l) {
+  float a = sm.own_neg[x][p][c], rel = sm.own_rel[x][p][c];
+  if (a != a) {
+    a = neg + lref;
+    rel = neg < -kNoMax ? -lref : neg;           // that of a column that has seen nothing stays so
+  }
+  float now = 0.0f, top = -INFINITY, most = -INFINITY, sum = 0.0f;
+  auto pass = [&](auto each) {
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass > 0) {
-      float before = sm.own_neg[x][p][c];
-      if (before != before) before = neg;
-      sm.own_top[x][p][c] = top;
-      group_pair_sync(1 + 4 * x + (c >> 5));
-      const float now = fminf(before, -fmaxf(sm.own_top[x][0][c], sm.own_top[x][1][c]) - lref);
-      sm.own_neg[x][p][c] = now;
-      base = now + lref;
-      l *= ex2(base - (before + lref));
-    }
-#pragma unroll 1
-    for (int k0 = 0; k0 < 64; k0 += 16) {
-      uint32_t u[16];
-      tmem_ld16(scores + k0, u);
+    for (int k0 = 0; k0 < 64; k0 += 32) {
+      uint32_t u[32];
+      tmem_ld32(scores + k0, u);
       tmem_ld_wait();
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
+      for (int k = 0; k < 32; ++k) {
         asm volatile("" : "+r"(u[k]));           // not before the wait
-        const float z = k0 + k < seen ? __fmul_rn(__uint_as_float(u[k]), fs) : -INFINITY;
-        if (pass == 0) top = fmaxf(top, z);
-        else sum += ex2(z + base);
+        const float z = __fmul_rn(__uint_as_float(u[k]), fs) + now;
+        u[k] = __float_as_uint(k0 + k < seen ? z : -INFINITY);
       }
+      each(k0, u);
     }
+  };
+  pass([&](int, const uint32_t (&u)[32]) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(u[k]));
+  });
+  sm.own_top[x][p][c] = top;
+  group_pair_sync(1 + 4 * x + (c >> 5));
+  now = fminf(a, -fmaxf(sm.own_top[x][0][c], sm.own_top[x][1][c]));
+  pass([&](int, const uint32_t (&u)[32]) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      sum += ex2(__uint_as_float(u[k]));
+      most = fmaxf(most, __uint_as_float(u[k]) + lsv);
+    }
+  });
+  sm.pair[x][p][c] = most;
+  group_pair_sync(1 + 4 * x + (c >> 5));
+  most = fmaxf(sm.pair[x][0][c], sm.pair[x][1][c]);
+  const float shift = now - a, next = fminf(rel < -kNoMax ? rel - shift : rel, kTop - most);
+  pass([&](int k0, const uint32_t (&u)[32]) {
+    uint32_t y[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2)
+      y[k / 2] = f16x2_of(ex2(__uint_as_float(u[k]) + (lsv + next)), ex2(__uint_as_float(u[k + 1]) + (lsv + next)));
+    tmem_st16(scores + k0 / 2, y);
+    tmem_st_wait();
+  });
+  sm.own_neg[x][p][c] = now;
+  sm.own_rel[x][p][c] = next;
+  return make_float2(fmaf(l, ex2(shift), sum), ex2(shift + (next - rel)));
+}
+// The halves of a shared tile of columns, at least one of them such: their O's weights and the sum of both (x, y, z).
+template <int D>
+__device__ __noinline__ float4 far_join(Smem<D>& sm, int p, int c, float neg, float neg_b, float lref, float l, float lb) {
+  auto from = [&](float own, float rel, float n) {
+    return own == own ? make_float2(own, rel) : make_float2(n + lref, n < -kNoMax ? -lref : n);
+  };
+  const float2 a = from(sm.own_neg[0][p][c], sm.own_rel[0][p][c], neg), b = from(sm.own_neg[1][0][c], sm.own_rel[1][0][c], neg_b);
+  float4 w = make_float4(1.0f, 0.0f, l, 0.0f);
+  float2 both = a;
+  if (lb != 0.0f) {
+    const float d = (b.x - a.x) + (b.y - a.y);
+    both.x = fminf(a.x, b.x);
+    both.y = d < 0.0f ? (b.x - both.x) + b.y : (a.x - both.x) + a.y;
+    w = make_float4(ex2(fminf(d, 0.0f)), ex2(-fmaxf(d, 0.0f)), fmaf(lb, ex2(both.x - b.x), l * ex2(both.x - a.x)), 0.0f);
   }
-  return l + sum;
+  sm.own_neg[0][p][c] = both.x;
+  sm.own_rel[0][p][c] = both.y;
+  return w;
 }
 // y of the page's keys where maxima are large (kKv8Large), over the S that it came from; their sum.
 __device__ __noinline__ float large_probabilities(uint32_t scores, int seen, float fs, float lsv, float neg) {
@@ -632,16 +676,21 @@ struct Softmax {
         for (;;) {
           if (moves) {
             const bool far = lsv == INFINITY;
-            if (far) lsv = t.own[p];
-            sm.pair[x][p][c] = largest(seen, fs, lsv);
+            if (!far) sm.pair[x][p][c] = largest(seen, fs, lsv);
             ok = wait(&sm.pv_done[x], (n & 1) ^ 1) && ok;             // O of the tiles before is complete
             if (either(!ok)) return;
             tc_fence_after();
-            const float top = fmaxf(sm.pair[x][0][c], sm.pair[x][1][c]);
-            const float now = fminf(neg, kTop - top), corr = ex2(now - neg);
-            if (far) l = own_sum(sm, scores, x, p, c, seen, fs, neg, lref, l);   // the tile is here: both warps say so
-            else l *= corr;
-            neg = now;
+            float corr;
+            if (far) {                           // the tile is here, so both warps say so
+              const float2 r = far_tile(sm, scores, x, p, c, seen, fs, t.own[p], neg, lref, l);
+              l = r.x;
+              corr = r.y;
+            } else {
+              const float now = fminf(neg, kTop - fmaxf(sm.pair[x][0][c], sm.pair[x][1][c]));
+              corr = ex2(now - neg);
+              neg = now;
+              l *= corr;
+            }
             if (n > n0) {                        // a half of the dims each
 #pragma unroll 1
               for (int d = p * (D / 2); d < (p + 1) * (D / 2); d += 16) {
@@ -652,6 +701,12 @@ struct Softmax {
                 for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * corr);
                 tmem_st16(out + d, u);
               }
+            }
+            if (far) {
+              tmem_ld32(scores, y);
+              arrived(y);
+              sum = 0.0f;                        // l has the tile already
+              break;
             }
           }
           sum = masked ? probabilities<true>(seen, fs, neg + lsv, y) : probabilities<false>(seen, fs, neg + lsv, y);
@@ -693,30 +748,35 @@ struct Softmax {
       sm.pair[x][p][c] = l;
       if (either(!ok)) return;
       l = sm.pair[x][0][c] + sm.pair[x][1][c];
-      float neg_l = sm.own_neg[x][p][c];
-      if (neg_l != neg_l) neg_l = neg;
       float own = 1.0f, others = 0.0f;           // weights of the halves' O
       if (joint) {
         const float2 b = sm.joined[0][c];
-        const float lb = b.y + sm.joined[1][c].y, now = fminf(neg, b.x);
-        own = ex2(now - neg);
-        others = lb == 0.0f ? 0.0f : ex2(now - b.x);
-        float nb = sm.own_neg[1][0][c];
-        if (nb != nb) nb = b.x;
-        const float least = fminf(neg_l, nb);
-        l *= ex2(least - neg_l);
-        if (lb != 0.0f) l = fmaf(lb, ex2(least - nb), l);
-        neg_l = least;
-        neg = now;
+        const float lb = b.y + sm.joined[1][c].y, na = sm.own_neg[0][p][c], nb = sm.own_neg[1][0][c];
+        if (na == na || nb == nb) {
+          const float4 w = far_join(sm, p, c, neg, b.x, lref, l, lb);
+          own = w.x;
+          others = w.y;
+          l = w.z;
+        } else {
+          const float now = fminf(neg, b.x);
+          own = ex2(now - neg);
+          others = lb == 0.0f ? 0.0f : ex2(now - b.x);
+          l = lb == 0.0f ? l * own : fmaf(lb, others, l * own);
+          neg = now;
+        }
       }
       const bool two = __any_sync(0xFFFFFFFFu, others != 0.0f);
       tc_fence_after();
       const int slot = w.t0 > 0 ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1;
-      // l and O count from neg_l and neg; by halves, as all of the difference may pass fp32's range
-      const float up = ex2(0.5f * (neg_l - neg));
-      own *= up;
-      others *= up;
-      const float m = -(neg_l + lref), f = l == 0.0f ? 0.0f : pow2((int)lref) * up / l;
+      float m = -(neg + lref), up = pow2((int)lref);
+      const float own_neg = sm.own_neg[x][p][c];
+      if (own_neg == own_neg) {                  // by halves, as all of the difference may pass fp32's range
+        m = -own_neg;
+        up = ex2(-0.5f * sm.own_rel[x][p][c]);
+        own *= up;
+        others *= up;
+      }
+      const float f = l == 0.0f ? 0.0f : up / l;
       if (col < cols && p == 0) {
         if (whole) {
           const size_t row = (size_t)(gr.r0 + in_group) * a.heads * a.G + w.h * a.G + (col - in_group * a.G);

@@ -115,3 +115,33 @@ def test_drafts_rejected_time_and_again(seed):
     assert np.array_equal(s.pool.cpu().numpy(), pool)
     assert np.array_equal(s.codes.cpu().numpy(), codes) and np.array_equal(s.scale.cpu().numpy(), scale)
     assert np.array_equal(s.tail.float().cpu().numpy(), tail)
+
+
+@gpu
+@pytest.mark.parametrize("rows,G", [(1, 4), (1, 16), (1, 32), (4, 7), (20, 8), (9, 33)])
+@pytest.mark.parametrize("scale", [1.0, 1e3, 1e6, 1e20])
+@pytest.mark.parametrize("n", [120, 700])
+def test_large_logits_beside_far_scales(rows, G, scale, n):
+    """The value of the one key above all others, to the last bits, whatever its page's scale and the others' are."""
+    d = 64
+    rng = np.random.default_rng(rows + G + n)
+    k = bf16(np.sign(rng.standard_normal((n, 1, d))) * 30.0)
+    for span in (0, 5, 25):
+        v = bf16(rng.standard_normal((n, 1, d)) * 10.0 ** rng.uniform(-span, span, -(-n // 64))[np.arange(n) // 64][:, None, None])
+        if span == 5:
+            v[64:128] = 0
+        best = rng.integers(0, n - rows, (rows, G))
+        q = bf16(np.sign(k[best, 0]) * 30.0)
+        s = Device(csa, Cache(1, [n], 1, d, tokens=[(k, v)]))
+        pos = list(range(n - rows, n))
+        out, lse = s.attend([0] * rows, pos, q, scale=scale)
+        assert s.flags == (0, 0)
+        from kv8_ref import head_entries
+        key, val, _ = head_entries(s.pool.cpu().numpy(), s.c.table[0], 0, d, np.arange(-(-n // 64)))
+        for r in range(rows):
+            x = (q[r].astype(np.float64) @ key[:pos[r] + 1].T) * scale
+            assert (x.argmax(-1) == best[r]).all()
+            # the others' weights are 2^-5000 and less
+            want = val[best[r]]
+            assert (np.abs(out[r] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -18 * np.abs(want).max(-1, keepdims=True)).all(), (span, r)
+            assert (np.abs(lse[r] - x.max(-1)) <= 2.0 ** -17 * x.max(-1)).all()

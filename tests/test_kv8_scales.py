@@ -231,3 +231,12 @@ def test_waits_that_run_out_among_far_scales(rows, G, budget):
         csa.csa_set_wait_budget(0)
     again, lse2 = s.attend([0] * rows, pos, q)
     assert s.flags == (0, 0) and np.array_equal(out, again) and np.array_equal(lse, lse2)
+
+
+@gpu
+@pytest.mark.parametrize("rows,G", [(160, 8), (96, 16), (70, 33), (40, 5)])
+def test_far_scales_in_segments_of_many_tiles(rows, G):
+    """More work than there are CTAs: each has whole segments, tile after tile of them far from the first."""
+    n, scales = 1400, [1, 1e-3, 0, 1e12, 1, 1e-9, 1, 0, 1e20, 1e-20]
+    for climbs in ([0.0], bits(np.array([0, 3, 9, -40, 0, 25, -80]), 64)):
+        run(rows + G, n, rows, G, 64, scales, climbs, kv=3)

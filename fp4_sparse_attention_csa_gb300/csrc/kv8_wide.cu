@@ -519,7 +519,8 @@ __device__ __noinline__ float large_probabilities(uint32_t scores, int seen, flo
       for (int j = 0; j < 2; ++j) {
         asm volatile("" : "+r"(u[k + j]));       // not before the wait
         // as `largest` rounds it; kTop minus the maximum is rounded, too, by up to 8
-        z[j] = k0 + k + j < seen ? ex2(fminf(fmaf(__uint_as_float(u[k + j]), fs, lsv) + neg, 15.0f)) : 0.0f;
+        const float t = fmaf(__uint_as_float(u[k + j]), fs, lsv) + neg;
+        z[j] = k0 + k + j < seen ? ex2(t > 15.0f ? 15.0f : t) : 0.0f;            // what is no number stays so
         sum += z[j];
       }
       y[k / 2] = f16x2_of(z[0], z[1]);

@@ -118,6 +118,30 @@ def test_drafts_rejected_time_and_again(seed):
 
 
 @gpu
+@pytest.mark.parametrize("rows,G", [(1, 4), (4, 7), (3, 16), (20, 8), (9, 33)])
+@pytest.mark.parametrize("scale", [1.0, 1e6, 1e12])
+@pytest.mark.parametrize("at", [3, 400, 690])
+def test_no_number_among_logits_of_any_size(rows, G, scale, at):
+    """Rows that see a token with a NaN or an infinity become NaN, and no others, beside small logits and large ones,
+    alike scales and far ones."""
+    d, n = 64, 700
+    rng = np.random.default_rng(at)
+    for far in (False, True):
+        k, v = bf16(rng.standard_normal((n, 1, d)) * 30), bf16(rng.standard_normal((n, 1, d)))
+        if far:
+            v = bf16(v * 10.0 ** rng.integers(-9, 9, -(-n // 64))[np.arange(n) // 64][:, None, None])
+        k[at, 0, 7], v[at + 1, 0, 3] = np.nan, np.inf
+        s = Device(csa, Cache(2, [n], 1, d, tokens=[(k, v)]))
+        pos = [int(x) for x in np.concatenate([np.arange(n - rows, n), np.arange(at - 2, at + 3)]) if x >= 0]
+        q = bf16(rng.standard_normal((len(pos), G, d)) * 30)
+        out, lse = s.attend([0] * len(pos), pos, q, scale=scale)
+        assert s.flags == (0, 0)
+        sees = np.array(pos) >= at
+        assert np.isnan(out[sees]).all() and np.isnan(lse[sees]).all()
+        assert np.isfinite(out[~sees]).all() and np.isfinite(lse[~sees]).all()
+
+
+@gpu
 @pytest.mark.parametrize("rows,G", [(1, 4), (1, 16), (1, 32), (4, 7), (20, 8), (9, 33)])
 @pytest.mark.parametrize("scale", [1.0, 1e3, 1e6, 1e20])
 @pytest.mark.parametrize("n", [120, 700])

@@ -17,7 +17,8 @@
 // The softmax's sum is l = sum of y / sv, in units of a power of two near 1 / sv.  That holds while a
 // segment's value scales lie within kKv8Near of its first tile's; from the first page on that does not, or
 // has no values at all (a scale of 0), the sum is formed with a maximum and powers of two of its own,
-// l = sum of 2^(s - ms): y may have none of a key that the sum is made of, and the other way round.
+// l = sum of 2^(s - ms): y may have none of a key that the sum is made of, and the other way round.  What y
+// is taken against is then held relative to ms.
 // The key scale, the query's power of two and the softmax scale are the logit's factor.
 //
 // Work: the tiles of all segments, in row and head order, are one list; CTA i takes the i-th
@@ -78,8 +79,8 @@ struct Smem {
   uint8_t pad[D == 64 && kBehind < 4096 ? 4096 - kBehind : 16];
   int first_pos[X::kStages][2];                  // position of a page's first slot; INT_MAX: no page
   float factor[COLS];                            // of a column's logits (log2 units)
-  float neg_m[COLS];                             // kTop minus the running maximum
-  float neg_l[COLS];                             // minus the sums' own maximum, once scales are far apart
+  float neg_m[COLS];                             // kTop minus the running maximum; once scales are far apart, beside neg_l
+  float neg_l[COLS];                             // minus the sums' own maximum by then
   int far, large;                                // a page's scale is, in this tile; a column's maximum is (kKv8Large)
   float red[4][COLS];                            // per warp: maxima of a tile, sums of p
   float corr[COLS];                              // correction of a column whose maximum moved; at the end 1 / l

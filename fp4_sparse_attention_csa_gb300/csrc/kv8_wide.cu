@@ -21,13 +21,13 @@
 // halves' lanes are the same columns, so a reads b's O in tensor memory as it is).
 //
 // What bounds it.  A tile of 128 keys and 2 x 128 columns of 128 dims is 32 MMAs of 65 clocks, 2080.
-// Four prompts of 512 rows, 32 heads over 8, after 8k to 16k tokens take 309 us for 392 GFLOP, 1.27 PFLOP/s
-// or 0.65 of the measured bf16 rate, where the queries' second part is work on top; the tensor pipe is
+// Four prompts of 512 rows, 32 heads over 8, after 8k to 16k tokens take 310 us for 392 GFLOP, 1.26 PFLOP/s
+// or 0.64 of the measured bf16 rate, where the queries' second part is work on top; the tensor pipe is
 // active for 54 %, issue slots 53 %.  A tile takes some 2700 clocks, and shared memory's port is what it
 // waits for: the products read 8 KB an MMA for S and 4 KB for O, 192 KB a tile, the conversion of the values
 // moves 48 KB and the copies 32 KB, 2125 clocks at 128 bytes.  (Without any power of two, for a
 // measurement, prompts took 302 us instead of 303.)  A step between segments takes 20 thousand, a share's search 10 thousand.  32
-// requests of 6 rows and 7 queries a key head, 42 columns of 64 dims, take 52.5 us: half of the
+// requests of 6 rows and 7 queries a key head, 42 columns of 64 dims, take 53 us: half of the
 // warps have columns that no query has.
 // Eight softmax warps, a thread a column, took 330 and 69 us; two issuing warps were slower, as were one that
 // sleeps at its barriers (366 against 347 us then) and one loop for both kinds of segments (326 against
